@@ -355,15 +355,62 @@ int mk_attention_decode_noalloc(const uint16_t* q, const uint16_t* k_t, const ui
  * cudaMemcpyToSymbol of 4 bytes. */
 int mk_attention_noalloc_status(void* stream);
 
-/* Limit, in nanoseconds, of every device-side wait of mk_attention_decode and
- * mk_attention_decode_noalloc calls issued after this one (process-wide; default 2e9).  Must
+/* Limit, in nanoseconds, of every device-side wait of mk_attention_decode,
+ * mk_attention_decode_noalloc and mk_tree_attention calls issued after this one (process-wide; default 2e9).  Must
  * be > 0. */
 int mk_attention_set_wait_timeout_ns(uint64_t ns);
 /* Test hook for failure detection (process-wide): while unit >= 0, the split-KV attention
  * kernels launched afterwards never load the 64-key unit with that global index (head h's units
  * are h * ceil(L/64) ..), so the compute warp waiting for it runs out of time and the call's
- * status reports MK_ERR_DEVICE_TIMEOUT.  Nothing faults or traps.  unit < 0 switches it off. */
+ * status reports MK_ERR_DEVICE_TIMEOUT.  In mk_tree_attention, block `unit` of the grid loads no
+ * keys.  Nothing faults or traps.  unit < 0 switches it off. */
 int mk_attention_debug_drop_unit(int unit);
+
+/* ---- Speculative decoding -------------------------------------------------------------------
+ * A step drafts a tree of up to n nodes per sequence.  Node 0 is the sequence's last token, whose
+ * key and value are not in the cache yet; nodes 1.. are drafted tokens.  parents: device int32
+ * [B][n], parents[b][i] in [-1, i): the node that node i follows (-1: none; a chain is -1, 0, 1,
+ * ..).  n_nodes: device int32 [B], the nodes of each sequence in use (clamped to 0..n; NULL: all
+ * n); rows of outputs behind them are left as they were.  lens: device int32 [B], cache rows of
+ * the sequence (clamped to 0..max_seq).  Node i's key and value stand at cache row lens[b] + i;
+ * nodes that do not fit the cache count as not in use.  The arrays are read on the device: the
+ * calls can be captured into a graph and replayed with new contents.  Device ids, positions and
+ * parents out of range never lead outside the buffers. */
+#define MK_BF16 0
+#define MK_FP16 1
+#define MK_FP32 2
+#define MK_MAX_TREE_NODES 256
+
+/* Sizes and element strides of a tree attention.  The last axis (head_dim values) is contiguous;
+ * every stride is a multiple of 8 elements (the stride of an axis of length 1 is not used). */
+typedef struct mk_tree_shape {
+  int dtype; /* MK_BF16 or MK_FP16: q, k, v and o */
+  int B, n, n_q_heads, n_kv_heads, head_dim, max_seq;
+  int64_t q_seq, q_node, q_head; /* q[b][i][h][..] */
+  int64_t k_seq, k_head, k_row;  /* k[b][h][row][..], 0 <= row < max_seq */
+  int64_t v_seq, v_head, v_row;
+  int64_t o_seq, o_node, o_head; /* o[b][i][h][..] */
+} mk_tree_shape;
+
+/* Attention of every node over the sequence's cache rows, the node's ancestors and itself:
+ *   o[b][i][h] = sum_j softmax_j(scale * q[b][i][h] . k[b][h / G][j]) v[b][h / G][j],
+ *   j in {0 .. lens[b] - 1} and lens[b] + a for a = i, parents[b][i], its parent, ..
+ * with G = n_q_heads / n_kv_heads.  n = 1 is decode attention over lens[b] + 1 rows.  Softmax and
+ * sums in fp32; the softmax weights are rounded to the inputs' type for the product with v.  k and
+ * v: one layer of the decoder's cache, or any such arrays.  Rows that a node does not see have no
+ * influence on it, whatever they hold; infinities and NaN in rows that it sees reach its output.
+ * A node whose parents are not a tree's (parents[b][i] outside [-1, i), or such an ancestor) gets
+ * zeros.  Requirements: head_dim 64 or 128; n_q_heads % n_kv_heads == 0, G <= 128; 1 <= n <=
+ * MK_MAX_TREE_NODES; q, k, v and o 16-byte aligned; scale finite and not 0.  No workspace; calls
+ * may overlap on different streams. */
+int mk_tree_attention(const mk_tree_shape* shape, const void* q, const void* k, const void* v, void* o,
+                      const int32_t* parents, const int32_t* n_nodes, const int32_t* lens, float scale,
+                      void* stream);
+/* Synchronise `stream` and report whether any mk_tree_attention call on the current device since
+ * the previous mk_tree_attention_status had a device wait run out (MK_ERR_DEVICE_TIMEOUT: its
+ * output is undefined; cleared by this call) or not (MK_OK).  The limit of the waits is
+ * mk_attention_set_wait_timeout_ns's. */
+int mk_tree_attention_status(void* stream);
 
 /* Last error text for ctx (or the thread's last context-free error when ctx is NULL). */
 const char* mk_last_error(const mk_ctx* ctx);

@@ -33,6 +33,10 @@ MK_ERR_NOT_RESIDENT = -4
 MK_ERR_STATE = -5
 MK_ERR_UNSUPPORTED = -6
 MK_MAX_BATCH = 16
+MK_BF16 = 0
+MK_FP16 = 1
+MK_FP32 = 2
+MK_MAX_TREE_NODES = 256
 MK_DISPATCH_STATIC = 0
 MK_DISPATCH_CLAIM = 1
 MK_DISPATCH_CLAIM_PACED = 2
@@ -71,6 +75,13 @@ class mk_graph_info(ctypes.Structure):
                 ("weight_bytes_per_step", ctypes.c_uint64), ("smem_bytes", ctypes.c_uint64)]
 
 
+class mk_tree_shape(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("dtype", "B", "n", "n_q_heads", "n_kv_heads", "head_dim",
+                                                  "max_seq")] + \
+        [(name, ctypes.c_int64) for name in ("q_seq", "q_node", "q_head", "k_seq", "k_head", "k_row",
+                                             "v_seq", "v_head", "v_row", "o_seq", "o_node", "o_head")]
+
+
 _vp, _i32, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
 _SIGS = {
     "mk_build_taskgraph": ([ctypes.POINTER(mk_config), _i32, ctypes.POINTER(_vp)], _i32),
@@ -106,6 +117,9 @@ _SIGS = {
     "mk_attention_noalloc_status": ([_vp], _i32),
     "mk_attention_set_wait_timeout_ns": ([_u64], _i32),
     "mk_attention_debug_drop_unit": ([_i32], _i32),
+    "mk_tree_attention": ([ctypes.POINTER(mk_tree_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp],
+                          _i32),
+    "mk_tree_attention_status": ([_vp], _i32),
     "mk_last_error": ([_vp], ctypes.c_char_p),
     "mk_destroy": ([_vp], None),
 }
@@ -357,6 +371,85 @@ def mk_attention_set_wait_timeout_ns(ns: int):
 
 def mk_attention_debug_drop_unit(unit: int):
     _check(_lib.mk_attention_debug_drop_unit(int(unit)))
+
+
+# ---- speculative decoding: these take torch tensors and read sizes, strides and types off them
+
+def _refuse(msg):
+    raise MkError(MK_ERR_INVALID_ARG, msg)
+
+
+def _dtype_code(t, what):
+    """MK_BF16 / MK_FP16 / MK_FP32 of a tensor; int16 holds bf16 bits (Megakernel.kv_view)."""
+    name = str(t.dtype)
+    code = {"torch.bfloat16": MK_BF16, "torch.int16": MK_BF16, "torch.float16": MK_FP16,
+            "torch.float32": MK_FP32}.get(name)
+    if code is None:
+        _refuse(f"{what}: {name} is not supported")
+    return code
+
+
+def _index_ptr(t, shape, what):
+    """data_ptr of a contiguous tensor of `shape` (None: NULL); indices are int32, the rest fp32."""
+    if t is None:
+        return None
+    want = "torch.float32" if what in ("u", "r", "temperature", "draft_temperature") else "torch.int32"
+    if tuple(t.shape) != shape or str(t.dtype) != want or not t.is_contiguous():
+        _refuse(f"{what} must be a contiguous {want} tensor of shape {shape}")
+    return t.data_ptr()
+
+
+class _on_device:
+    """The tensors' device made current for the call (they all have to be on it)."""
+
+    def __init__(self, first, *others):
+        dev = first.device
+        for t in others:
+            if t is not None and t.device != dev:
+                _refuse(f"tensors on {dev} and {t.device}")
+        if dev.type != "cuda":
+            _refuse(f"tensors must be on a CUDA device, not {dev}")
+        import torch
+        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def mk_tree_attention(q, k, v, o, parents, n_nodes, lens, scale: float, stream=None):
+    """Attention of drafted trees over a cache.  q, o: [B, n, n_q_heads, head_dim]; k, v: [B,
+    n_kv_heads, max_seq, head_dim] (e.g. ``kv_view()[layer, 0]`` and ``[layer, 1]``); bf16 or
+    fp16, any strides with a contiguous last axis; parents [B, n], lens [B] and n_nodes [B] (or
+    None) int32."""
+    if q.dim() != 4 or k.dim() != 4 or o.shape != q.shape or v.shape != k.shape:
+        _refuse("q and o must be [B, n, n_q_heads, head_dim], k and v [B, n_kv_heads, max_seq, head_dim]")
+    B, n, hq, d = q.shape
+    if k.shape[0] != B or k.shape[3] != d:
+        _refuse("q and k differ in batch or head_dim")
+    code = _dtype_code(q, "q")
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
+    for t, what, st in ((q, "q", qs), (k, "k", ks), (v, "v", vs), (o, "o", os_)):
+        if _dtype_code(t, what) != code:
+            _refuse("q, k, v and o must have one type")
+        if st[3] != 1:
+            _refuse(f"{what}: the last axis must be contiguous")
+    sh = mk_tree_shape(code, B, n, hq, k.shape[1], d, k.shape[2], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
+                       vs[0], vs[1], vs[2], os_[0], os_[1], os_[2])
+    with _on_device(q, k, v, o, parents, n_nodes, lens):
+        _check(_lib.mk_tree_attention(ctypes.byref(sh), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                      _index_ptr(parents, (B, n), "parents"), _index_ptr(n_nodes, (B,), "n_nodes"),
+                                      _index_ptr(lens, (B,), "lens"), scale, _stream(stream)))
+
+
+def mk_tree_attention_status(stream=None) -> int:
+    """MK_OK, or MK_ERR_DEVICE_TIMEOUT if a tree attention since the last status call had a device
+    wait run out (returned, not raised)."""
+    return _lib.mk_tree_attention_status(_stream(stream))
 
 
 def mk_last_error(ctx=None) -> str:

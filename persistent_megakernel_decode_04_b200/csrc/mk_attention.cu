@@ -568,6 +568,8 @@ std::atomic<int> g_attn_drop_unit{-1};                   // test hook (see mk_at
 
 void attention_set_wait_timeout_ns(uint64_t ns) { g_attn_timeout_ns.store(ns); }
 void attention_debug_drop_unit(int unit) { g_attn_drop_unit.store(unit); }
+uint64_t attention_wait_timeout_ns() { return g_attn_timeout_ns.load(); }
+int attention_drop_unit() { return g_attn_drop_unit.load(); }
 
 int attention_decode(const uint16_t* q, const uint16_t* k_t, const uint16_t* v, float* o, int BH, int d, int L,
                      float scale, void* workspace, cudaStream_t stream, int n_sms, uint32_t* err_word,

@@ -2074,6 +2074,48 @@ int mk_attention_status(void* workspace, int BH, int d, int L, void* stream) {
   return fail(nullptr, MK_ERR_DEVICE_TIMEOUT, "attention wait timed out");
 }
 
+int mk_tree_attention(const mk_tree_shape* shape, const void* q, const void* k, const void* v, void* o,
+                      const int32_t* parents, const int32_t* n_nodes, const int32_t* lens, float scale,
+                      void* stream) {
+  if (!shape || !q || !k || !v || !o || !parents || !lens) return fail(nullptr, MK_ERR_INVALID_ARG, "NULL operand");
+  mk_tree_shape s = *shape;
+  if (s.dtype != MK_BF16 && s.dtype != MK_FP16)
+    return fail(nullptr, MK_ERR_INVALID_ARG, "tree attention takes MK_BF16 or MK_FP16");
+  if (s.B < 1 || s.n < 1 || s.n > MK_MAX_TREE_NODES || s.max_seq < 1 || (s.head_dim != 64 && s.head_dim != 128))
+    return fail(nullptr, MK_ERR_INVALID_ARG, "bad B, n, max_seq or head_dim");
+  if (s.n_kv_heads < 1 || s.n_q_heads < 1 || s.n_q_heads % s.n_kv_heads || s.n_q_heads / s.n_kv_heads > 128)
+    return fail(nullptr, MK_ERR_INVALID_ARG, "n_q_heads must be 1..128 times n_kv_heads");
+  if (!std::isfinite(scale) || scale == 0.f) return fail(nullptr, MK_ERR_INVALID_ARG, "scale must be finite and not 0");
+  for (const void* p : {q, k, v, (const void*)o})
+    if (reinterpret_cast<uintptr_t>(p) & 15) return fail(nullptr, MK_ERR_INVALID_ARG, "q, k, v and o must be 16-byte aligned");
+  struct Axis {
+    int64_t* stride;
+    int size;
+  };
+  const Axis axes[] = {{&s.q_seq, s.B},  {&s.q_node, s.n},        {&s.q_head, s.n_q_heads}, {&s.o_seq, s.B},
+                       {&s.o_node, s.n}, {&s.o_head, s.n_q_heads}, {&s.k_seq, s.B},         {&s.k_head, s.n_kv_heads},
+                       {&s.k_row, s.max_seq}, {&s.v_seq, s.B},    {&s.v_head, s.n_kv_heads}, {&s.v_row, s.max_seq}};
+  for (const Axis& a : axes) {
+    if (a.size == 1) *a.stride = s.head_dim;  // not used; a valid value for the tensor maps
+    if (*a.stride <= 0 || *a.stride % 8 || *a.stride >= (1ll << 39))
+      return fail(nullptr, MK_ERR_INVALID_ARG, "strides must be positive multiples of 8 elements, below 2^39");
+  }
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fail(nullptr, MK_ERR_CUDA, "no CUDA device");
+  std::string err;
+  const int rc = tree_attention(s, q, k, v, o, parents, n_nodes, lens, scale, n, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(nullptr, rc, err);
+  return MK_OK;
+}
+
+int mk_tree_attention_status(void* stream) {
+  std::string err;
+  const int rc = tree_attention_status(reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(nullptr, rc, err);
+  return MK_OK;
+}
+
 int mk_attention_noalloc_status(void* stream) {
   std::string err;
   const int rc = attention_noalloc_status(reinterpret_cast<cudaStream_t>(stream), &err);

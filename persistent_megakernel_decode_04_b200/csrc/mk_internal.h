@@ -219,6 +219,15 @@ int attention_decode_noalloc(const uint16_t* q, const uint16_t* k_t, const uint1
 int attention_noalloc_status(cudaStream_t stream, std::string* err);
 void attention_set_wait_timeout_ns(uint64_t ns);
 void attention_debug_drop_unit(int unit);
+uint64_t attention_wait_timeout_ns();
+int attention_drop_unit();
+
+// Speculative decoding (mk_tree_attention.cu, mk_tree_verify.cu, mk_cache.cu).  Arguments were
+// checked by the C entry points.
+int tree_attention(const mk_tree_shape& s, const void* q, const void* k, const void* v, void* o,
+                   const int32_t* parents, const int32_t* n_nodes, const int32_t* lens, float scale, int n_sms,
+                   cudaStream_t stream, std::string* err);
+int tree_attention_status(cudaStream_t stream, std::string* err);
 
 // Prefill (mk_prefill.cu).
 struct PrefillParams {

@@ -11,12 +11,15 @@
 // TMA writes them with the 128-byte swizzle.  128 rows cost the same as 1: a 128-key tile takes
 // the tensor cores 2 x 0.13 us, while its 64 KB take an SM's share of HBM 1.4 us.
 //
-// Two streams of four softmax warps each keep the tensor cores and the loads fed: with one row
-// tile the streams take alternate key tiles, each with its own running maximum, sum and O; with
-// two row tiles (more than 128 rows) stream w is row tile w and every key tile serves both.
+// A block holds one row tile (two blocks per SM, so that one block's start, end and softmax run
+// beside the other's loads and products) or, for more than 128 rows, two row tiles that share
+// every key tile (one block per SM: half the reads from L2).  Each row tile has four softmax
+// warps; one warp issues the loads, one the products, and two helpers prepare the tree: the
+// ancestor bits of every node, and V tiles that end the sequence.
+//
 // The keys of a (sequence, KV head, row tiles) unit are split over a thread-block cluster, whose
-// CTAs merge their partial results through distributed shared memory: no workspace, no atomics,
-// a fixed order of summation.
+// blocks merge their partial results through distributed shared memory: no workspace, no
+// atomics, a fixed order of summation.
 //
 // Precision.  S, the softmax statistics and O are fp32.  P is rounded to the inputs' 16-bit type
 // for the second product (relative 2^-9 / 2^-12, the size of the output's own rounding).  The
@@ -28,7 +31,6 @@
 #include <math.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "mk_internal.h"
 #include "mk_ptx.cuh"
@@ -38,24 +40,26 @@ namespace tree {
 
 constexpr int kKeys = 128;        // keys per tile
 constexpr int kRows = 128;        // rows per row tile
-constexpr int kSoftWarps = 8;     // two streams of four
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
 constexpr int kMaxNodes = MK_MAX_TREE_NODES;
 constexpr int kAncStride = kMaxNodes / 32 + 1;  // odd: rows fall on different banks
 constexpr int kMaxCluster = 16;
-constexpr uint32_t kTmemCols = 512;  // S0 S1 at 0, 128 (P over their first 64), O0 O1 at 256, 256 + D
+constexpr int kCh = 32;            // keys of a row of S in registers at a time
 
-template <int D>
+// NT: row tiles of a block (1 or 2).
+template <int D, int NT>
 struct Geo {
+  static constexpr int kSoft = 8 * NT;             // softmax warps; then loads, products, two helpers
+  static constexpr int kThreads = (kSoft + 4) * 32;
   static constexpr int kTile = kKeys * D * 2;      // bytes of a K, V or Q tile
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = (NT == 1 ? 2 : 4) * (128 / D) + (NT == 1 && D == 64 ? 1 : 0);
   static constexpr int kOStride = D + 4;           // floats: 16-byte rows, no bank conflicts
-  static constexpr int kData = 2 * kTile + kStages * kTile;
-  // more than half of an SM's shared memory, so that one CTA runs per SM: a second one would
-  // wait for TMEM columns while its cluster's other CTAs hold theirs
-  static_assert(kData > 116 * 1024, "one CTA per SM");
-  static_assert(2 * kRows * kOStride * 4 <= kData, "partial O fits over Q and the ring");
+  static constexpr int kData = (NT + kStages) * kTile;
+  // Tensor memory: S_w at w * 128 (P over it: keys 0..63 at 0, 64..127 at 64), O_w at NT * 128 + w * D
+  static constexpr uint32_t kCols = NT * 256;
+  // Shared memory bounds the blocks per SM to 512 / kCols: one more would wait for tensor memory
+  // while its cluster's other blocks hold theirs.
+  static_assert(NT == 1 ? kData > 76 * 1024 : kData > 116 * 1024, "blocks per SM");
+  static_assert(NT * kRows * kOStride * 4 <= kData, "partial O fits over Q and the ring");
 };
 
 struct Params {
@@ -66,19 +70,26 @@ struct Params {
   int64_t q_seq, q_node, q_head, o_seq, o_node, o_head, v_seq, v_head, v_row;
   int n, hq, hkv, G, max_seq;
   int nt;        // nodes per row tile
-  int mt, mp;    // row tiles, units of up to two row tiles
+  int units;     // blocks' worth of row tiles per (sequence, KV head)
+  uint32_t inv_g;  // r / G = r * inv_g >> 16 for r < 256
   float c;       // |scale| * log2(e)
-  uint32_t flip; // sign bits flipped in q: scale < 0
+  uint32_t negate; // scale < 0: the product takes -Q (a bit of the instruction descriptor)
   uint64_t timeout_ns;
   int drop_block;  // test hook: the block that issues no loads (-1: none)
 };
 
 struct Ctl {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], q_full, mma_done;
-  uint32_t tmem, abort, bad_v, pad;
-  float m[2][kRows], l[2][kRows];
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full, q_full, mma_done, anc_full;
+  uint32_t tmem, abort;
+  uint32_t bad_v;  // infinite or NaN values among the drafts that this block saw
+  // Counters that only grow, for roles that may be more than one step apart (an mbarrier's parity
+  // cannot tell two steps from none): V tiles to clean that were issued; helpers' shares done.
+  uint32_t v_issued, v_clean;
+  uint32_t bad_any;  // some block of the cluster has bad_v set
+  float pair[2][2][2 * kRows];  // what the two threads of a row tell each other, by turns
+  // (maximum, sum) of every row that this block finishes from every block of the cluster
+  float2 stat[2 * kRows + kMaxCluster];
   uint32_t anc[kMaxNodes * kAncStride];
-  int16_t up[2][kMaxNodes];
 };
 
 __device__ uint32_t g_err;  // first wait that ran out since the last status call
@@ -104,6 +115,27 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Param
 // For a whole warp: every lane gets the same answer, as the warp-wide tcgen05 forms need.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Params& P, Ctl& S) {
   return __all_sync(0xffffffffu, wait(bar, parity, P, S));
+}
+
+// Wait until a growing counter has reached `value`, with the same limit.
+__device__ __forceinline__ bool wait_count(const uint32_t* at, uint32_t value, const Params& P, Ctl& S) {
+  if ((int32_t)(ld_acquire_cta_shared(at) - value) >= 0) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while ((int32_t)(ld_acquire_cta_shared(at) - value) < 0) {
+    if (*reinterpret_cast<volatile uint32_t*>(&S.abort)) return false;
+    if (globaltimer_ns() - t0 > P.timeout_ns) {
+      *reinterpret_cast<volatile uint32_t*>(&S.abort) = 1;
+      atomicExch(&g_err, 1u);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_count_warp(const uint32_t* at, uint32_t value, const Params& P, Ctl& S) {
+  return __all_sync(0xffffffffu, wait_count(at, value, P, S));
+}
+__device__ __forceinline__ void count_up(uint32_t* at) {
+  asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(at)) : "memory");
 }
 
 __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -161,6 +193,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       MK_I8(r, 24), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15};" ::MK_I8(r, 0), MK_I8(r, 8), "r"(taddr)
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t* r) {
+  if constexpr (N == 16)
+    tmem_st16(taddr, r);
+  else
+    tmem_st32(taddr, r);
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -198,15 +243,11 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_peer_f2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 __device__ __forceinline__ float4 ld_peer_f4(uint32_t addr) {
   float4 v;
@@ -216,10 +257,8 @@ __device__ __forceinline__ float4 ld_peer_f4(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
@@ -242,281 +281,282 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t* anc, int rel0) {
   return __funnelshift_r(anc[w], hi, rel0 & 31);
 }
 
-// The position in load order of key tile j's K and V: K runs `ahead` tiles before V.
-__device__ __forceinline__ int k_index(int j, int ahead) { return j < ahead ? j : 2 * j - ahead + 1; }
-__device__ __forceinline__ int v_index(int j, int ahead, int T) { return j + min(T, j + ahead); }
+// Ancestor bits (self included) of nodes 0..nn-1, one warp, 32 nodes at a time.  Within the block
+// of 32 by doubling: a node takes over the bits of the node it points at, and then points where
+// that one points.  What it points at then lies in an earlier block, whose bits are complete.
+// `next`: the parent of node `lane`.
+__device__ __forceinline__ void ancestors(const int32_t* parents, int next, int nn, uint32_t* anc, int lane) {
+  for (int base = 0; base < nn; base += 32) {
+    const int i = base + lane;
+    int up = next;
+    next = i + 32 < nn ? parents[i + 32] : -1;
+    bool live = i < nn && up >= -1 && up < i;  // else not a tree's: the node sees nothing
+    uint32_t own = live ? 1u << lane : 0u;
+    if (!live) up = -1;
+    while (__any_sync(0xffffffffu, up >= base)) {
+      const int src = up >= base ? up - base : lane;
+      const uint32_t bits = __shfl_sync(0xffffffffu, own, src);
+      const int further = __shfl_sync(0xffffffffu, up, src);
+      const bool ok = __shfl_sync(0xffffffffu, (int)live, src);
+      if (up >= base) {
+        own |= bits, up = further;
+        if (!ok) live = false, own = 0, up = -1;
+      }
+    }
+    uint32_t* mine = anc + i * kAncStride;
+    if (up >= 0 && !(anc[up * kAncStride + (up >> 5)] >> (up & 31) & 1)) live = false;
+#pragma unroll
+    for (int k = 0; k < kMaxNodes / 32; ++k) {
+      uint32_t w = live && up >= 0 && k * 32 < base ? anc[up * kAncStride + k] : 0u;
+      if (k * 32 == base && live) w = own;
+      mine[k] = w;
+    }
+    __syncwarp();
+  }
+}
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kThreads, 1)
+// Whether a node's parents are a tree's (its own bit is set then).
+__device__ __forceinline__ bool alive(const Ctl& S, int node) {
+  return S.anc[node * kAncStride + (node >> 5)] >> (node & 31) & 1;
+}
+
+// Infinite and NaN values of drafts that the node sees, added to n output values at `out`.
+template <bool FP16>
+__device__ __noinline__ void add_nonfinite(const Params& P, const Ctl& S, int b, int h, int len, int node, int col,
+                                           int n, uint16_t* out) {
+  if (!alive(S, node)) return;
+  for (int a = 0; a <= node; ++a) {
+    if (!(S.anc[node * kAncStride + (a >> 5)] >> (a & 31) & 1)) continue;
+    const uint16_t* val = P.v + (int64_t)b * P.v_seq + (int64_t)h * P.v_head + (int64_t)(len + a) * P.v_row + col;
+    for (int x = 0; x < n; ++x)
+      if (nonfinite16<FP16>(val[x]))
+        out[x] = (uint16_t)pack16<FP16>(value16<FP16>(out[x]) + value16<FP16>(val[x]), 0.f);
+  }
+}
+
+// Output rows that this block finishes: row r's partial results, weighted, from the C blocks.
+// The loops are kept rolled: this runs once, and its instructions come from memory.
+template <int D, bool FP16, int NT>
+__device__ __forceinline__ void merge(const Params& P, const Ctl& S, const uint8_t* data, int b, int h, int first,
+                                      int rows, int per, int rank, int C, int len, int warp, int lane) {
+  using Ge = Geo<D, NT>;
+  constexpr int kLanes = D / 4, kPer = 32 / kLanes;  // lanes per row, rows per warp side by side
+  const int sub = lane / kLanes, in = lane % kLanes, col = in * 4;
+  const int r0 = rank * per, r1 = min(rows, r0 + per), tile_rows = P.nt * P.G;
+  if (r0 >= r1) return;
+#pragma unroll 1
+  for (int base = r0 + warp * kPer; base < r1; base += Ge::kThreads / 32 * kPer) {
+    const int r = min(base + sub, r1 - 1);
+    // lane p of the row's group holds part p's weight (C <= 16 <= kLanes)
+    const float2 st = S.stat[(r - r0) * C + (in & (C - 1))];
+    float mx = st.x;
+    for (int off = C / 2; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    // a part that saw no key has no O to read
+    float f = st.x == -INFINITY && st.y == 0.f ? 0.f : mx == -INFINITY ? 1.f : ex2((st.x - mx) * P.c);
+    float sum = st.y * f;
+    for (int off = C / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const int t = NT == 2 && r >= tile_rows, lr = r - t * tile_rows;
+    const int local = (int)(lr * P.inv_g >> 16), g = lr - local * P.G, node = first + t * P.nt + local;
+    f = sum == 0.f || !alive(S, node) ? 0.f : __fdividef(f, sum);
+    const uint32_t src = smem_u32(data) + (uint32_t)(((t * kRows + lr) * Ge::kOStride + col) * 4);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int p0 = 0; p0 < C; p0 += 8) {
+      float fp[8];
+      float4 v[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {  // eight loads in flight
+        fp[p] = __shfl_sync(0xffffffffu, f, p0 + p, kLanes);
+        v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p0 + p >= C) fp[p] = 0.f;
+        if (fp[p] != 0.f) v[p] = ld_peer_f4(mapa(src, p0 + p));
+      }
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        acc[0] = fmaf(fp[p], v[p].x, acc[0]);
+        acc[1] = fmaf(fp[p], v[p].y, acc[1]);
+        acc[2] = fmaf(fp[p], v[p].z, acc[2]);
+        acc[3] = fmaf(fp[p], v[p].w, acc[3]);
+      }
+    }
+    if (base + sub >= r1) continue;
+    uint16_t* out = P.o + (int64_t)b * P.o_seq + (int64_t)node * P.o_node + (int64_t)(h * P.G + g) * P.o_head + col;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack16<FP16>(acc[0], acc[1]), pack16<FP16>(acc[2], acc[3]));
+    if (S.bad_any) add_nonfinite<FP16>(P, S, b, h, len, node, col, 4, out);
+  }
+}
+
+template <int D, bool FP16, int NT>
+__global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
     tree_attention(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ Params P) {
-  using Ge = Geo<D>;
+  using Ge = Geo<D, NT>;
   extern __shared__ uint8_t raw[];
   __shared__ Ctl S;
+  constexpr int kTmaWarp = Ge::kSoft, kMmaWarp = Ge::kSoft + 1, kHelper = Ge::kSoft + 2;
   uint8_t* data = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t* ring = data + 2 * Ge::kTile;
+  uint8_t* ring = data + NT * Ge::kTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
 
-  const int unit = blockIdx.x / C;
-  const int pair = unit % P.mp, h = (unit / P.mp) % P.hkv, b = unit / P.mp / P.hkv;
-  const int len = min(max(P.lens[b], 0), P.max_seq);
-  const int nn = min(min(P.n_nodes ? max(P.n_nodes[b], 0) : P.n, P.n), P.max_seq - len);
-  if (pair * 2 * P.nt >= nn) return;  // no node here (the whole cluster alike)
-  const int tiles = min(2, P.mt - pair * 2) == 2 && (pair * 2 + 1) * P.nt < nn ? 2 : 1;
-  const int total = len + nn, T_all = (total + kKeys - 1) / kKeys;
-  const int t0 = (int)((int64_t)rank * T_all / C), T = (int)((int64_t)(rank + 1) * T_all / C) - t0;
-  const int ahead = tiles == 2 ? 1 : 2;  // K tiles loaded before the first V tile
+  const int unit = blockIdx.x / C, head = unit / P.units;
+  const int b = head / P.hkv, h = head - b * P.hkv;
+  const int first = (unit - head * P.units) * NT * P.nt;  // first node of the block's row tiles
+  int len = P.lens[b], nn = P.n_nodes ? P.n_nodes[b] : P.n;
+  // softmax warps: row tile, row, and which half of a tile's keys (and of O's columns) of that row
+  const int w = warp >> 3, row = tid & 127, half = (warp >> 2) & 1;
+  const int local = (int)(row * P.inv_g >> 16);
 
-  if (tid == 0) {
-    for (int i = 0; i < Ge::kStages; ++i) {
-      mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], 1);
+  // ---- start: whatever does not need the lengths first ----
+  int parent = -1;
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+#pragma unroll 1
+      for (int i = 0; i < Ge::kStages; ++i) {
+        mbar_init(&S.full[i], 1);
+        mbar_init(&S.empty[i], 1);
+      }
+#pragma unroll 1
+      for (int i = 0; i < NT; ++i) {
+        mbar_init(&S.s_full[i], 1);
+        mbar_init(&S.p_full[i], 8);
+      }
+      mbar_init(&S.o_full, 1);
+      mbar_init(&S.q_full, Ge::kSoft);
+      mbar_init(&S.mma_done, 1);
+      mbar_init(&S.anc_full, 1);
+      S.abort = S.bad_v = S.bad_any = S.v_issued = S.v_clean = 0;
+      fence_mbar_init();
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 4);
-      mbar_init(&S.o_full[i], 1);
-    }
-    mbar_init(&S.q_full, kSoftWarps);
-    mbar_init(&S.mma_done, 1);
-    S.abort = 0;
-    S.bad_v = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMmaWarp) {
-    tc_alloc(&S.tmem, kTmemCols);
+  } else if (warp == kMmaWarp) {
+    tc_alloc(&S.tmem, Ge::kCols);
     tc_relinquish();
+  } else if (warp == kHelper) {
+    if (lane < P.n) parent = P.parents[(int64_t)b * P.n + lane];
+  } else if (warp < Ge::kSoft) {
+    // Q rows into the swizzled tile: 16-byte piece c of row r goes to piece c ^ (r % 8).  Rows of
+    // the tile without a node keep what is there: they only reach their own, unused, results.
+    const int x0 = tid & 255, c = x0 % (D / 8), used = min(P.nt, P.n - first - w * P.nt) * P.G;
+    const uint16_t* src = P.q + (int64_t)b * P.q_seq + (int64_t)(first + w * P.nt) * P.q_node +
+                          (int64_t)h * P.G * P.q_head + c * 8;
+    const uint32_t dst = smem_u32(data) + w * Ge::kTile + (c / 8) * kRows * 128;
+#pragma unroll 1
+    for (int r = x0 / (D / 8); r < used; r += 2 * kRows / (D / 8)) {
+      const int lr = (int)(r * P.inv_g >> 16);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + r * 128 + ((c & 7) ^ (r & 7)) * 16),
+                   "l"(src + (int64_t)lr * P.q_node + (int64_t)(r - lr * P.G) * P.q_head)
+                   : "memory");
+    }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (C > 1) cluster_arrive();  // every block of the cluster has started: waited for before the first access
   const uint32_t tmem = S.tmem;
 
+  len = min(max(len, 0), P.max_seq), nn = min(min(max(nn, 0), P.n), P.max_seq - len);
+  const bool on = first < nn;                      // else there is no node here (the whole cluster alike)
+  const bool two = NT == 2 && first + P.nt < nn;   // the second row tile has nodes
+  const int T_all = on ? (len + nn + kKeys - 1) / kKeys : 0;
+  const int t0 = rank * T_all / C, T = (rank + 1) * T_all / C - t0;
+  const int edge = max(0, len / kKeys - t0);  // first tile of this block that has rows behind len
+  const int rows = min(nn - first, NT * P.nt) * P.G, per = (rows + C - 1) / C;  // rows; of these to finish
+
   if (warp == kTmaWarp) {
-    // ---- loads: K and V tiles in the order in which the products consume them ----
-    if (lane == 0) {
-      int x = 0;  // loads issued
-      auto load = [&](const CUtensorMap* map, int tile) {
+    // ---- loads: K and V of a tile in turn ----
+    if (lane == 0 && (int)blockIdx.x != P.drop_block) {
+      int x = 0;
+#pragma unroll 1
+      for (; x < 2 * T; ++x) {
         const int stage = x % Ge::kStages, use = x / Ge::kStages;
-        if (use > 0 && !wait(&S.empty[stage], (use - 1) & 1, P, S)) return false;
+        if (use > 0 && !wait(&S.empty[stage], (use - 1) & 1, P, S)) break;
         mbar_arrive_expect_tx(&S.full[stage], Ge::kTile);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          tma_4d(ring + stage * Ge::kTile + c * kKeys * 128, map, c * 64, (t0 + tile) * kKeys, h, b, &S.full[stage]);
-        ++x;
-        return true;
-      };
-      bool ok = (int)blockIdx.x != P.drop_block;
-      int k = 0;
-      for (; ok && k < min(T, ahead); ++k) ok = load(&map_k, k);
-      for (int v = 0; ok && v < T; ++v) {
-        ok = load(&map_v, v);
-        if (ok && k < T) ok = load(&map_k, k++);
+          tma_4d(ring + stage * Ge::kTile + c * kKeys * 128, x & 1 ? &map_v : &map_k, c * 64, (t0 + (x >> 1)) * kKeys,
+                 h, b, &S.full[stage]);
+        if ((x & 1) && (x >> 1) >= edge) count_up(&S.v_issued);
       }
-      if (*reinterpret_cast<volatile uint32_t*>(&S.abort))  // leave no copy in flight
+      if (x < 2 * T)  // given up: leave no copy in flight
         for (int y = max(0, x - Ge::kStages); y < x; ++y)
           wait_slow(&S.full[y % Ge::kStages], (y / Ge::kStages) & 1, P.timeout_ns, S, true);
     }
   } else if (warp == kMmaWarp) {
-    // ---- products, in an order that keeps one stream's product beside the other's softmax ----
-    if (lane == 0) {
+    // ---- products: one row tile's beside the other's (or the other block's) softmax ----
+    if (lane == 0 && T > 0) {
       constexpr uint32_t type = FP16 ? 0u : 1u;
       constexpr uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(kRows >> 4) << 24);
-      constexpr uint32_t idesc_s = idesc | ((uint32_t)(kKeys >> 3) << 17);
+      const uint32_t idesc_s = idesc | P.negate | ((uint32_t)(kKeys >> 3) << 17);
       constexpr uint32_t idesc_o = idesc | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
       const uint32_t q_base = smem_u32(data), ring_base = smem_u32(ring);
-      const int n0 = tiles == 2 ? T : (T + 1) / 2, n1 = tiles == 2 ? T : T / 2;
-      bool ok = T > 0 && wait(&S.q_full, 0, P, S);
+      const int last = two ? 1 : 0;
+      bool ok = wait(&S.q_full, 0, P, S);
       tc_fence_after();
-      auto scores = [&](int w, int it) {  // S_w = Q K^T of the stream's it-th tile
-        const int j = tiles == 2 ? it : 2 * it + w, x = k_index(j, ahead), stage = x % Ge::kStages;
-        if (!wait(&S.full[stage], (x / Ge::kStages) & 1, P, S)) return false;
-        tc_fence_after();
-        const uint32_t a = q_base + (tiles == 2 ? w : 0) * Ge::kTile, bb = ring_base + stage * Ge::kTile;
+      // step y = -1 .. T - 1, for each row tile t: O_t += P_t V of tile y, then S_t = Q_t K^T of tile y + 1
+#pragma unroll 1
+      for (int y = -last - 1; ok && y < (last + 1) * T; ++y) {
+        const int t = (y + last + 1) & last, j = last ? y >> 1 : y;
+        if (j >= 0) {
+          const int x = 2 * j + 1, stage = x % Ge::kStages;
+          ok = wait(&S.full[stage], (x / Ge::kStages) & 1, P, S) &&
+               (j < edge || wait_count(&S.v_clean, 2 * (j - edge + 1), P, S)) && wait(&S.p_full[t], j & 1, P, S);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t bb = ring_base + stage * Ge::kTile;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s / 4) * kKeys * 128 + (s % 4) * 32;
-          tc_mma_f16(tmem + w * kKeys, desc128(a + off, 16, 1024), desc128(bb + off, 16, 1024), idesc_s, s != 0);
+          for (int s = 0; s < kKeys / 16; ++s)
+            mma_ts(tmem + NT * kKeys + t * D, tmem + t * kKeys + (s & 4) * 16 + (s & 3) * 8, desc128(bb + s * 2048, kKeys * 128, 1024),
+                   idesc_o, j != 0 || s != 0);
+          if (t == last) tc_commit(&S.empty[stage]);
         }
-        tc_commit(&S.s_full[w]);
-        if (tiles == 1 || w == 1) tc_commit(&S.empty[stage]);
-        return true;
-      };
-      auto output = [&](int w, int it) {  // O_w += P_w V
-        const int j = tiles == 2 ? it : 2 * it + w, x = v_index(j, ahead, T), stage = x % Ge::kStages;
-        if (!wait(&S.full[stage], (x / Ge::kStages) & 1, P, S)) return false;
-        if (!wait(&S.p_full[w], it & 1, P, S)) return false;
-        // both streams have cleaned their halves of a tile that ends the sequence
-        if (tiles == 2 && w == 0 && (t0 + j + 1) * kKeys > len && !wait(&S.p_full[1], it & 1, P, S)) return false;
-        tc_fence_after();
-        const uint32_t bb = ring_base + stage * Ge::kTile;
+        if (j + 1 < T) {
+          const int x = 2 * j + 2, stage = x % Ge::kStages;
+          ok = wait(&S.full[stage], (x / Ge::kStages) & 1, P, S);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = q_base + t * Ge::kTile, bb = ring_base + stage * Ge::kTile;
 #pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s)
-          mma_ts(tmem + 256 + w * D, tmem + w * kKeys + s * 8, desc128(bb + s * 2048, kKeys * 128, 1024), idesc_o,
-                 it != 0 || s != 0);
-        if (tiles == 1 || w == 1) tc_commit(&S.empty[stage]);
-        return true;
-      };
-      if (ok) ok = scores(0, 0);
-      if (ok && n1 > 0) ok = scores(1, 0);
-      for (int it = 0; ok && it < n0; ++it) {
-        ok = output(0, it);
-        if (ok && it + 1 < n0) ok = scores(0, it + 1);
-        if (ok && it + 1 == n0) tc_commit(&S.o_full[0]);
-        if (ok && it < n1) {
-          ok = output(1, it);
-          if (ok && it + 1 < n1) ok = scores(1, it + 1);
-          if (ok && it + 1 == n1) tc_commit(&S.o_full[1]);
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (s / 4) * kKeys * 128 + (s % 4) * 32;
+            tc_mma_f16(tmem + t * kKeys, desc128(a + off, 16, 1024), desc128(bb + off, 16, 1024), idesc_s, s != 0);
+          }
+          tc_commit(&S.s_full[t]);
+          if (t == last) tc_commit(&S.empty[stage]);
         }
       }
+      if (ok) tc_commit(&S.o_full);
       tc_commit(&S.mma_done);  // nothing in flight when TMEM is freed
       wait_slow(&S.mma_done, 0, P.timeout_ns, S, true);
     }
-  } else {
-    // ---- softmax: one thread per row ----
-    const int w = warp >> 2, row = tid & 127;
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    // Q rows into the swizzled tiles: 16-byte piece c of row r goes to piece c ^ (r % 8)
-    {
-      const int pieces = D / 8;
-      for (int x = tid; x < tiles * kRows * pieces; x += kSoftWarps * 32) {
-        const int t = x / (kRows * pieces), r = (x / pieces) % kRows, c = x % pieces;
-        const int node = (pair * 2 + t) * P.nt + r / P.G;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (r < P.nt * P.G && node < nn) {
-          val = *reinterpret_cast<const uint4*>(P.q + (int64_t)b * P.q_seq + (int64_t)node * P.q_node +
-                                                (int64_t)(h * P.G + r % P.G) * P.q_head + c * 8);
-          val.x ^= P.flip, val.y ^= P.flip, val.z ^= P.flip, val.w ^= P.flip;
-        }
-        *reinterpret_cast<uint4*>(data + t * Ge::kTile + (c / 8) * kRows * 128 + r * 128 +
-                                  ((c & 7) ^ (r & 7)) * 16) = val;
-      }
-      fence_proxy_async_smem();
+  } else if (warp >= kHelper) {
+    // ---- helpers: the tree, and V tiles that end the sequence ----
+    if (on && warp == kHelper) {
+      ancestors(P.parents + (int64_t)b * P.n, parent, nn, S.anc, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full);
+      if (lane == 0) mbar_arrive(&S.anc_full);
     }
-    // Ancestor bits of every node by doubling: in each round a node takes over the bits of the
-    // node it points at and then points where that one points.
-    {
-      const int i = tid;  // 256 threads, kMaxNodes nodes
-      int up = -1;
-      bool live = i < nn;
-      if (live) {
-        up = P.parents[(int64_t)b * P.n + i];
-        if (up < -1 || up >= i) live = false, up = -1;  // not a tree's: the node sees nothing
-      }
+    // 0 x inf and 0 x NaN must not reach rows that do not see the key: rows behind the last node
+    // become zero, and so do infinite and NaN values of drafts (their own descendants get them
+    // back at the end).
+#pragma unroll 1
+    for (int j = edge; j < T; ++j) {
+      const int x = 2 * j + 1, stage = x % Ge::kStages;
+      if (!wait_count_warp(&S.v_issued, j - edge + 1, P, S)) break;
+      if (!wait_warp(&S.full[stage], (x / Ge::kStages) & 1, P, S)) break;
+      uint4* tile = reinterpret_cast<uint4*>(ring + stage * Ge::kTile);
+      const int key0 = (t0 + j) * kKeys, from = max(0, len - key0);
+      const int drafts = min(kKeys, len + nn - key0);  // keys from .. drafts - 1 are drafts
+      // each helper takes every other group of four keys: 8 pieces of 16 bytes per key and half
+#pragma unroll 1
+      for (int key = (from & ~3) + (warp - kHelper) * 4 + lane / 8; key < kKeys; key += 8) {
+        if (key < from) continue;
 #pragma unroll
-      for (int k = 0; k < kMaxNodes / 32; ++k) S.anc[i * kAncStride + k] = live && (i >> 5) == k ? 1u << (i & 31) : 0u;
-      S.up[0][i] = (int16_t)(live ? up : -2);
-      named_bar_sync(1, kSoftWarps * 32);
-      for (int rnd = 0;; ++rnd) {
-        const int cur = S.up[rnd & 1][i];
-        uint32_t add[kMaxNodes / 32];
-        int nxt = cur;
-        if (cur >= 0) {
-          nxt = S.up[rnd & 1][cur];
-#pragma unroll
-          for (int k = 0; k < kMaxNodes / 32; ++k) add[k] = S.anc[cur * kAncStride + k];
-        }
-        // the barrier with a vote: also the end, once no node points at another
-        int more;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-            "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-            : "=r"(more)
-            : "r"((int)(cur >= 0))
-            : "memory");
-        if (!more) break;
-        if (cur >= 0) {
-#pragma unroll
-          for (int k = 0; k < kMaxNodes / 32; ++k)
-            S.anc[i * kAncStride + k] = nxt == -2 ? 0u : S.anc[i * kAncStride + k] | add[k];
-        }
-        S.up[(rnd + 1) & 1][i] = (int16_t)nxt;
-        named_bar_sync(1, kSoftWarps * 32);
-      }
-    }
-    const int node = (pair * 2 + (tiles == 2 ? w : 0)) * P.nt + row / P.G;
-    const bool real = row < P.nt * P.G && node < nn;
-    const uint32_t* anc = S.anc + (real ? node : 0) * kAncStride;
-    const bool dead = real && !(anc[node >> 5] >> (node & 31) & 1);  // its parents are not a tree's
-    const int count = tiles == 2 ? T : w == 0 ? (T + 1) / 2 : T / 2;
-    constexpr float kBias = FP16 ? 7.f : 0.f;
-    float m = -INFINITY, l = 0.f;  // maximum that P is taken against; this row's sum of P
-    for (int it = 0; it < count; ++it) {
-      const int j = tiles == 2 ? it : 2 * it + w, key0 = (t0 + j) * kKeys;
-      if (!wait_warp(&S.s_full[w], it & 1, P, S)) break;
-      tc_fence_after();
-      uint32_t s[kKeys];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32(lane_base + w * kKeys + k * 32, s + k * 32);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_use32(s + k * 32);
-      const bool edge = key0 + kKeys > len;  // the tile has drafts, or rows behind the last one
-      if (edge || dead) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t see = dead ? 0u : visible32(anc, key0 + k * 32 - len);
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (!(see >> x & 1)) s[k * 32 + x] = 0xff800000u;
-        }
-      }
-      float mx[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
-#pragma unroll
-      for (int x = 4; x < kKeys; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
-      const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
-      const bool move = (top - m) * P.c > 8.f;  // also from -inf; false for -inf - -inf
-      if (__any_sync(0xffffffffu, move)) {
-        const float f = top == -INFINITY ? 1.f : ex2((m - top) * P.c);
-        m = top;
-        l *= f;
-        if (it > 0) {
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[32];
-            tmem_ld32(lane_base + 256 + w * D + k * 32, o);
-            tmem_wait_ld();
-            tmem_use32(o);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_st32(lane_base + 256 + w * D + k * 32, o);
-          }
-        }
-      }
-      const float nm = m == -INFINITY ? 0.f : kBias - m * P.c;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t p[kKeys / 2];
-#pragma unroll
-      for (int x = 0; x < kKeys / 2; ++x) {
-        const float a = ex2(fmaf(__uint_as_float(s[2 * x]), P.c, nm));
-        const float e = ex2(fmaf(__uint_as_float(s[2 * x + 1]), P.c, nm));
-        sum[(2 * x) & 3] += a;
-        sum[(2 * x + 1) & 3] += e;
-        p[x] = pack16<FP16>(a, e);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st32(lane_base + w * kKeys, p);
-      tmem_st32(lane_base + w * kKeys + 32, p + 32);
-      tmem_wait_st();
-      if (edge) {
-        // 0 x inf and 0 x NaN must not reach rows that do not see the key: rows behind the last
-        // node become zero, and so do infinite and NaN values of drafts (their own descendants
-        // get them back at the end).  The streams that use the tile share the work.
-        const int x = v_index(j, ahead, T), stage = x % Ge::kStages;
-        if (!wait_warp(&S.full[stage], (x / Ge::kStages) & 1, P, S)) break;
-        uint4* tile = reinterpret_cast<uint4*>(ring + stage * Ge::kTile);
-        const int part = tiles == 2 ? tid : row, step = tiles == 2 ? 256 : 128;
-        for (int y = part; y < Ge::kTile / 16; y += step) {
-          const int rel = key0 + (y / 8) % kKeys - len;  // 8 pieces of 16 bytes per key and half
-          if (rel < 0) continue;
+        for (int c = 0; c < D / 64; ++c) {
+          uint4* at = tile + (c * kKeys + key) * 8 + lane % 8;
           uint4 val = make_uint4(0, 0, 0, 0);
-          if (rel < nn) {
-            val = tile[y];
+          if (key < drafts) {
+            val = *at;
             uint32_t* e = reinterpret_cast<uint32_t*>(&val);
             bool bad = false;
 #pragma unroll
@@ -527,127 +567,187 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!bad) continue;
             S.bad_v = 1;
           }
-          tile[y] = val;
+          *at = val;
         }
-        fence_proxy_async_smem();
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) count_up(&S.v_clean);
+    }
+  } else {
+    // ---- softmax: two threads per row, one for each half of a tile's keys ----
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.q_full);
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lane_base + w * kKeys + half * 64, o_at = lane_base + NT * kKeys + w * D + half * (D / 2);
+    const int node = first + w * P.nt + local;
+    const bool real = local < P.nt && node < nn;
+    const bool any = __any_sync(0xffffffffu, real);  // else the warp's rows are left alone (their P is garbage)
+    const uint32_t* anc = S.anc + (real ? node : 0) * kAncStride;
+    const int count = w == 0 || two ? T : 0;
+    // the row's other thread: tell it x, get its x (turn: a slot is written again two turns later)
+    auto tell = [&](float x, int turn) {
+      S.pair[turn & 1][half][w * kRows + row] = x;
+      named_bar_sync(1 + w * 4 + (warp & 3), 64);
+      return S.pair[turn & 1][half ^ 1][w * kRows + row];
+    };
+    constexpr float kBias = FP16 ? 7.f : 0.f;
+    float m = -INFINITY, l = 0.f;  // maximum that P is taken against; sum of P over this thread's keys
+    bool ok = count == 0 || edge >= T || wait_warp(&S.anc_full, 0, P, S);
+#pragma unroll 1
+    for (int j = 0; j < count; ++j) {
+      ok = ok && wait_warp(&S.s_full[w], j & 1, P, S);
+      tc_fence_after();
+      if (any) {
+        // a row of S is read twice, kCh keys at a time: for the maximum, and for the weights
+        const int rel = (t0 + j) * kKeys + half * 64 - len;  // > -64: drafts, or rows behind the last one
+        auto scores = [&](int k, uint32_t* s) {
+          tmem_ld32(s_at + k * kCh, s);
+          tmem_wait_ld();
+          tmem_use32(s);
+          if (rel + k * kCh > -kCh) {
+            const uint32_t see = visible32(anc, rel + k * kCh);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!(see >> x & 1)) s[x] = 0xff800000u;
+          }
+        };
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int k = 0; k < 64 / kCh; ++k) {
+          uint32_t s[kCh];
+          scores(k, s);
+#pragma unroll
+          for (int x = 0; x < kCh; x += 4) {
+            mx[0] = fmaxf(mx[0], fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
+            mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])));
+          }
+        }
+        const float mine = fmaxf(mx[0], mx[1]);
+        const float top = fmaxf(fmaxf(mine, tell(mine, j)), m);
+        const bool move = real && (top - m) * P.c > 8.f;  // also from -inf; false for -inf - -inf
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = top == -INFINITY ? 1.f : ex2((m - top) * P.c);
+          m = top;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int k = 0; k < D / 64; ++k) {
+              uint32_t o[32];
+              tmem_ld32(o_at + k * 32, o);
+              tmem_wait_ld();
+              tmem_use32(o);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st32(o_at + k * 32, o);
+            }
+          }
+        }
+        const float nm = m == -INFINITY ? 0.f : kBias - m * P.c;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0; k < 64 / kCh; ++k) {
+          uint32_t s[kCh], p[kCh / 2];
+          scores(k, s);
+#pragma unroll
+          for (int x = 0; x < kCh / 2; ++x) {
+            float a0 = nm, a1 = nm;
+            fma2(a0, a1, __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), P.c, P.c);
+            a0 = ex2(a0), a1 = ex2(a1);
+            sum[0] += a0;
+            sum[1] += a1;
+            p[x] = pack16<FP16>(a0, a1);
+          }
+          tmem_st16(s_at + k * (kCh / 2), p);  // over scores that this thread has read
+        }
+        l += sum[0] + sum[1];
+        tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[w]);
     }
-    // ---- this CTA's partial result: statistics, and O over Q's and the ring's room ----
-    bool good = true;
-    if (tiles == 2 || T > 0) good = count == 0 || wait_warp(&S.o_full[w], 0, P, S);
-    if (T > 0 && (tiles == 2 || T > 1)) good = wait_warp(&S.o_full[w ^ 1], 0, P, S) && good;  // the ring is read out
+    // ---- the end: every product is done, Q and the ring are read out ----
+    if (T > 0) ok = ok && wait_warp(&S.o_full, 0, P, S);
     tc_fence_after();
-    S.m[w][row] = m;
-    S.l[w][row] = l;
-    if (good && count > 0) {
-      float* dst = reinterpret_cast<float*>(data) + (size_t)(w * kRows + row) * Ge::kOStride;
+    if (C > 1) cluster_wait();
+    if (any) {
+      l += tell(l, count);
+      if (C == 1) {
+        if (ok) ok = wait_warp(&S.anc_full, 0, P, S);
+        const float inv = l == 0.f || !real || !alive(S, node) ? 0.f : 1.f / l;
+        uint16_t* out = P.o + (int64_t)b * P.o_seq + (int64_t)node * P.o_node +
+                        (int64_t)(h * P.G + row - local * P.G) * P.o_head + half * (D / 2);
+#pragma unroll 1
+        for (int k = 0; k < D / 64; ++k) {
+          uint32_t o[32];
+          tmem_ld32(o_at + k * 32, o);
+          tmem_wait_ld();
+          tmem_use32(o);
+          if (real)
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t o[32];
-        tmem_ld32(lane_base + 256 + w * D + k * 32, o);
-        tmem_wait_ld();
-        tmem_use32(o);
+            for (int x = 0; x < 32; x += 8) {
+              uint32_t p[4];
 #pragma unroll
-        for (int x = 0; x < 32; x += 4)
-          *reinterpret_cast<uint4*>(dst + k * 32 + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+              for (int y = 0; y < 4; ++y) {
+                const float f0 = __uint_as_float(o[x + 2 * y]), f1 = __uint_as_float(o[x + 2 * y + 1]);
+                p[y] = inv == 0.f ? 0u : pack16<FP16>(f0 * inv, f1 * inv);
+              }
+              *reinterpret_cast<uint4*>(out + k * 32 + x) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+        }
+        if (S.bad_v && real) add_nonfinite<FP16>(P, S, b, h, len, node, half * (D / 2), D / 2, out);
+      } else {
+        // this block's partial result: O over Q's and the ring's room, and each row's statistics to
+        // the block that finishes the row
+        if (real && half == 0) {
+          const int r = w * P.nt * P.G + row, owner = r / per;
+          st_peer_f2(mapa(smem_u32(&S.stat[(r - owner * per) * C + rank]), owner), m, l);
+          if (S.bad_v) st_peer_u32(mapa(smem_u32(&S.bad_any), owner), 1);
+        }
+        if (count > 0) {
+          float* dst = reinterpret_cast<float*>(data) + (size_t)(w * kRows + row) * Ge::kOStride + half * (D / 2);
+#pragma unroll 1
+          for (int k = 0; k < D / 64; ++k) {
+            uint32_t o[32];
+            tmem_ld32(o_at + k * 32, o);
+            tmem_wait_ld();
+            tmem_use32(o);
+            if (real)
+#pragma unroll
+              for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<uint4*>(dst + k * 32 + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          }
+        }
       }
     }
     tc_fence_before();
   }
   __syncwarp();
-  cluster_sync();
-  tc_fence_after();
-  if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
-
-  // ---- merge: this CTA finishes a share of the rows, D / 4 lanes per row ----
-  if (warp < kSoftWarps) {
-    constexpr int kLanes = D / 4, kPer = 32 / kLanes;  // rows per warp at a time
-    const int first = pair * 2 * P.nt;
-    const int rows = (min(nn, first + tiles * P.nt) - first) * P.G;
-    const int per = (rows + C - 1) / C, r1 = min(rows, (rank + 1) * per);
-    const int parts = tiles == 2 ? C : 2 * C;
-    const int sub = lane / kLanes, col = (lane % kLanes) * 4;
-    uint32_t bad = 0;
-    for (int x = 0; x < C; ++x) bad |= ld_peer_u32(mapa(smem_u32(&S.bad_v), x));
-    for (int base = rank * per + warp * kPer; base < r1; base += kSoftWarps * kPer) {
-      const int r = base + sub;
-      const bool on = r < r1;
-      const int node = first + (on ? r : base) / P.G, g = (on ? r : base) % P.G;
-      const int t = (node - first) / P.nt, lr = (node - first - t * P.nt) * P.G + g;  // row tile, row in it
-      // lane x of the row's group looks after parts x, x + kLanes
-      float mx = -INFINITY, pm[2], pl[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int part = lane % kLanes + y * kLanes;
-        pm[y] = -INFINITY, pl[y] = 0.f;
-        if (part < parts) {
-          const int w = tiles == 2 ? t : part & 1, who = tiles == 2 ? part : part >> 1;
-          pm[y] = ld_peer_f32(mapa(smem_u32(&S.m[w][lr]), who));
-          pl[y] = ld_peer_f32(mapa(smem_u32(&S.l[w][lr]), who));
-        }
-        mx = fmaxf(mx, pm[y]);
-      }
-#pragma unroll
-      for (int off = kLanes / 2; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      float f[2], sum = 0.f;
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        // a part that saw no key has no O to read
-        f[y] = pm[y] == -INFINITY && pl[y] == 0.f ? 0.f : mx == -INFINITY ? 1.f : ex2((pm[y] - mx) * P.c);
-        sum += pl[y] * f[y];
-      }
-#pragma unroll
-      for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int p0 = 0; p0 < parts; p0 += 4) {
-        float fp[4];
-        float4 v[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {  // parts beyond the last have weight 0
-          const int part = p0 + y;
-          fp[y] = __shfl_sync(0xffffffffu, part < kLanes ? f[0] : f[1], part % kLanes, kLanes);
-          const int w = tiles == 2 ? t : part & 1, who = tiles == 2 ? part : part >> 1;
-          v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (fp[y] != 0.f)
-            v[y] = ld_peer_f4(
-                mapa(smem_u32(reinterpret_cast<float*>(data) + (size_t)(w * kRows + lr) * Ge::kOStride + col), who));
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          acc[0] = fmaf(fp[y], v[y].x, acc[0]);
-          acc[1] = fmaf(fp[y], v[y].y, acc[1]);
-          acc[2] = fmaf(fp[y], v[y].z, acc[2]);
-          acc[3] = fmaf(fp[y], v[y].w, acc[3]);
-        }
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) acc[x] *= inv;
-      if (bad && on) {  // infinite and NaN values of drafts that the node sees
-        for (int a = 0; a <= node; ++a) {
-          if (!(S.anc[node * kAncStride + (a >> 5)] >> (a & 31) & 1)) continue;
-          const uint16_t* src = P.v + (int64_t)b * P.v_seq + (int64_t)h * P.v_head + (int64_t)(len + a) * P.v_row + col;
-          for (int x = 0; x < 4; ++x)
-            if (nonfinite16<FP16>(src[x])) acc[x] += value16<FP16>(src[x]);
-        }
-      }
-      if (on)
-        *reinterpret_cast<uint2*>(P.o + (int64_t)b * P.o_seq + (int64_t)node * P.o_node +
-                                  (int64_t)(h * P.G + g) * P.o_head + col) =
-            make_uint2(pack16<FP16>(acc[0], acc[1]), pack16<FP16>(acc[2], acc[3]));
-    }
+  if (C > 1) {
+    if (warp >= Ge::kSoft) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
   }
-  __syncwarp();
-  cluster_sync();  // peers read this CTA's shared memory until here
+  tc_fence_after();
+  if (warp == kMmaWarp) tc_dealloc(tmem, Ge::kCols);
+  if (C > 1) {
+    if (on) merge<D, FP16, NT>(P, S, data, b, h, first, rows, per, rank, C, len, warp, lane);
+    __syncwarp();
+    cluster_arrive();  // peers read this block's shared memory until here
+    cluster_wait();
+  }
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, int NT>
 static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, const Params& P, int64_t units, int n_sms,
                           cudaStream_t stream) {
-  constexpr int kSmem = Geo<D>::kData + 1024;
+  constexpr int kSmem = Geo<D, NT>::kData + 1024;
+  const auto kernel = tree_attention<D, FP16, NT>;
   // the largest cluster that fits the device, found once per device: 16, or the portable 8
   static std::atomic<int> largest[64];
   int dev = 0;
@@ -657,21 +757,20 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, const P
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Geo<D, NT>::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int most = dev < 64 ? largest[dev].load() : 0;
   if (!most) {
-    e = cudaFuncSetAttribute(tree_attention<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(tree_attention<D, FP16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr[0].val.clusterDim.x = kMaxCluster;
     cfg.gridDim = dim3(kMaxCluster);
     int fit = 0;
-    if (cudaOccupancyMaxActiveClusters(&fit, tree_attention<D, FP16>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
       fit = 0;
     }
@@ -681,10 +780,20 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, const P
   // Keys are split while that gives idle SMs work, down to one tile per block.
   int C = 1;
   while (2 * C <= most && units * 2 * C <= n_sms && (int64_t)C * kKeys < P.max_seq) C *= 2;
-  if (units * C > 0x7fffffff) return cudaErrorInvalidValue;
   attr[0].val.clusterDim.x = C;
   cfg.gridDim = dim3((unsigned)(units * C));
-  return cudaLaunchKernelEx(&cfg, tree_attention<D, FP16>, mk_, mv, P);
+  return cudaLaunchKernelEx(&cfg, kernel, mk_, mv, P);
+}
+
+template <int D, bool FP16>
+static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params& P, int B, int n_sms,
+                          cudaStream_t stream) {
+  const int tiles = (P.n + P.nt - 1) / P.nt, NT = tiles > 1 ? 2 : 1;
+  P.units = (tiles + NT - 1) / NT;
+  const int64_t units = (int64_t)B * P.hkv * P.units;
+  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  return NT == 2 ? launch<D, FP16, 2>(mk_, mv, P, units, n_sms, stream)
+                 : launch<D, FP16, 1>(mk_, mv, P, units, n_sms, stream);
 }
 
 static bool encode(CUtensorMap* map, const void* base, int fp16, int D, int max_seq, int hkv, int B, int64_t seq,
@@ -715,10 +824,9 @@ int tree_attention(const mk_tree_shape& s, const void* q, const void* k, const v
   P.v_seq = s.v_seq, P.v_head = s.v_head, P.v_row = s.v_row;
   P.n = s.n, P.hq = s.n_q_heads, P.hkv = s.n_kv_heads, P.G = s.n_q_heads / s.n_kv_heads, P.max_seq = s.max_seq;
   P.nt = kRows / P.G;
-  P.mt = (s.n + P.nt - 1) / P.nt;
-  P.mp = (P.mt + 1) / 2;
+  P.inv_g = 65536u / P.G + 1;
   P.c = fabsf(scale) * 1.44269504088896340736f;
-  P.flip = scale < 0.f ? 0x80008000u : 0u;
+  P.negate = scale < 0.f ? 1u << 13 : 0u;
   P.timeout_ns = attention_wait_timeout_ns();
   P.drop_block = attention_drop_unit();
   const int fp16 = s.dtype == MK_FP16;
@@ -728,12 +836,11 @@ int tree_attention(const mk_tree_shape& s, const void* q, const void* k, const v
     *err = "cuTensorMapEncodeTiled failed for the cache (strides of 2^40 bytes or more?)";
     return MK_ERR_INVALID_ARG;
   }
-  const int64_t units = (int64_t)s.B * s.n_kv_heads * P.mp;
   cudaError_t e;
   if (s.head_dim == 128)
-    e = fp16 ? launch<128, true>(mk_, mv, P, units, n_sms, stream) : launch<128, false>(mk_, mv, P, units, n_sms, stream);
+    e = fp16 ? launch<128, true>(mk_, mv, P, s.B, n_sms, stream) : launch<128, false>(mk_, mv, P, s.B, n_sms, stream);
   else
-    e = fp16 ? launch<64, true>(mk_, mv, P, units, n_sms, stream) : launch<64, false>(mk_, mv, P, units, n_sms, stream);
+    e = fp16 ? launch<64, true>(mk_, mv, P, s.B, n_sms, stream) : launch<64, false>(mk_, mv, P, s.B, n_sms, stream);
   if (e != cudaSuccess) {
     *err = std::string("tree_attention launch: ") + cudaGetErrorString(e);
     return MK_ERR_CUDA;

@@ -412,6 +412,62 @@ int mk_tree_attention(const mk_tree_shape* shape, const void* q, const void* k, 
  * mk_attention_set_wait_timeout_ns's. */
 int mk_tree_attention_status(void* stream);
 
+/* Sizes and element strides of a verification; the last axis (vocab logits) is contiguous. */
+typedef struct mk_verify_shape {
+  int dtype; /* MK_FP32, MK_BF16 or MK_FP16: target and draft */
+  int B, n, vocab;
+  int64_t t_seq, t_node; /* target[b][i][..] */
+  int64_t d_seq, d_node; /* draft[b][i][..] (not used without draft) */
+} mk_verify_shape;
+
+/* Which drafted nodes the target model accepts, and the token that follows them: rejection
+ * sampling down the tree, lossless for the target's distribution.
+ *   target[b][i]: the target's logits after node i; draft[b][i]: the logits that node i's children
+ *   were drawn from, independently of each other (rows of nodes without children are not read), or
+ *   draft NULL: the drafts were picked for certain (e.g. the k likeliest), all with q = 1.
+ *   tokens: int32 [B][n] (a token outside the vocabulary has probability 0); u: fp32 [B][n] and
+ *   r: fp32 [B], uniform in [0, 1); temperature: fp32 [B] >= 0 for the target (NULL: 1; 0: greedy),
+ *   draft_temperature: fp32 [B] > 0 (NULL: 1).
+ * With p_i = softmax(target[b][i] / temperature), q_i likewise: P = p_0 and node 0 is current; the
+ * current node's children are asked in index order; child c is accepted if u[b][c] q(x_c) < P(x_c)
+ * and becomes current with P = p_c; otherwise P = max(P - q, 0) / its sum (P stays if nothing is
+ * left).  Then next_token is the first token whose cumulative P exceeds r.  At temperature 0, P is
+ * 1 at the largest logit's lowest index, and u, r and draft are not asked.
+ *   path: int32 [B][n], the accepted nodes from node 0 on, -1 behind them; n_path: int32 [B] their
+ *   count; next_token: int32 [B] (-1 where the last node's logits are no distribution: NaN,
+ *   infinite, or only -inf; children of such a node are not accepted; -1 with n_path 0 for a
+ *   sequence without nodes).
+ * Sums that a draw depends on are formed in 64 bits.  workspace: device scratch of
+ * mk_tree_verify_workspace_bytes, 16-byte aligned, its contents do not matter; calls that share it
+ * must not overlap (nor may replays of graphs that captured such calls).  Two launches. */
+size_t mk_tree_verify_workspace_bytes(int B, int n, int vocab);
+int mk_tree_verify(const mk_verify_shape* shape, const void* target, const void* draft, const int32_t* tokens,
+                   const int32_t* parents, const int32_t* n_nodes, const float* u, const float* r,
+                   const float* temperature, const float* draft_temperature, int32_t* path, int32_t* n_path,
+                   int32_t* next_token, void* workspace, void* stream);
+
+/* A cache in the decoder's layout, [layer][K|V][max_batch][n_kv_heads][max_seq][head_dim], 16-bit
+ * values, 16-byte aligned; the calls below work on its first B sequences. */
+typedef struct mk_cache_shape {
+  int n_layers, max_batch, B, n_kv_heads, max_seq, head_dim; /* head_dim 64 or 128 */
+} mk_cache_shape;
+
+/* Keep the accepted nodes of a tree step: in every layer, K and V, row lens[b] + path[b][j] moves to
+ * row lens[b] + j for j < n_path[b], and new_lens[b] = lens[b] + n_path[b].  path: int32 [B][n] with
+ * growing entries (as mk_tree_verify leaves them): a path ends at the first entry that is not above
+ * the one before it, not below n, or whose row is behind the cache.  Rows behind the kept ones hold
+ * what they held or a copy.  new_lens must not overlap lens. */
+int mk_cache_commit(const mk_cache_shape* shape, void* cache, const int32_t* path, int n, const int32_t* n_path,
+                    const int32_t* lens, int32_t* new_lens, void* stream);
+
+/* Sequences take over other sequences' rows (a prompt forked to several answers, beams): sequence
+ * b gets the first lens[src[b]] rows that sequence src[b] had before the call, in every layer, K and
+ * V, and new_lens[b] = lens[src[b]].  src: int32 [B], any map (forks, swaps, cycles); an entry
+ * outside [0, B) keeps the sequence as it is.  Rows behind those taken are left as they were.  B <=
+ * MK_MAX_BATCH; new_lens must not overlap lens. */
+int mk_cache_reorder(const mk_cache_shape* shape, void* cache, const int32_t* src, const int32_t* lens,
+                     int32_t* new_lens, void* stream);
+
 /* Last error text for ctx (or the thread's last context-free error when ctx is NULL). */
 const char* mk_last_error(const mk_ctx* ctx);
 void mk_destroy(mk_ctx* ctx);

@@ -82,6 +82,15 @@ class mk_tree_shape(ctypes.Structure):
                                              "v_seq", "v_head", "v_row", "o_seq", "o_node", "o_head")]
 
 
+class mk_verify_shape(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("dtype", "B", "n", "vocab")] + \
+        [(name, ctypes.c_int64) for name in ("t_seq", "t_node", "d_seq", "d_node")]
+
+
+class mk_cache_shape(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("n_layers", "max_batch", "B", "n_kv_heads", "max_seq", "head_dim")]
+
+
 _vp, _i32, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
 _SIGS = {
     "mk_build_taskgraph": ([ctypes.POINTER(mk_config), _i32, ctypes.POINTER(_vp)], _i32),
@@ -120,6 +129,10 @@ _SIGS = {
     "mk_tree_attention": ([ctypes.POINTER(mk_tree_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp],
                           _i32),
     "mk_tree_attention_status": ([_vp], _i32),
+    "mk_tree_verify_workspace_bytes": ([_i32, _i32, _i32], _sz),
+    "mk_tree_verify": ([ctypes.POINTER(mk_verify_shape)] + [_vp] * 14, _i32),
+    "mk_cache_commit": ([ctypes.POINTER(mk_cache_shape), _vp, _vp, _i32, _vp, _vp, _vp, _vp], _i32),
+    "mk_cache_reorder": ([ctypes.POINTER(mk_cache_shape), _vp, _vp, _vp, _vp, _vp], _i32),
     "mk_last_error": ([_vp], ctypes.c_char_p),
     "mk_destroy": ([_vp], None),
 }
@@ -450,6 +463,69 @@ def mk_tree_attention_status(stream=None) -> int:
     """MK_OK, or MK_ERR_DEVICE_TIMEOUT if a tree attention since the last status call had a device
     wait run out (returned, not raised)."""
     return _lib.mk_tree_attention_status(_stream(stream))
+
+
+def mk_tree_verify_workspace_bytes(B: int, n: int, vocab: int) -> int:
+    return _lib.mk_tree_verify_workspace_bytes(int(B), int(n), int(vocab))
+
+
+def mk_tree_verify(target, draft, tokens, parents, n_nodes, u, r, temperature, draft_temperature, path, n_path,
+                   next_token, workspace, stream=None):
+    """Which drafted nodes the target accepts, and the next token.  target, draft (or None):
+    logits [B, n, vocab] in fp32, bf16 or fp16 with a contiguous last axis; tokens, parents, path
+    [B, n], n_nodes (or None), n_path, next_token [B] int32; u [B, n], r, temperature,
+    draft_temperature [B] (the last two or None) fp32."""
+    if target.dim() != 3 or (draft is not None and draft.shape != target.shape):
+        _refuse("target and draft must be [B, n, vocab]")
+    B, n, V = target.shape
+    ts = target.stride()
+    ds = draft.stride() if draft is not None else ts
+    if ts[2] != 1 or ds[2] != 1:
+        _refuse("the logits' last axis must be contiguous")
+    code = _dtype_code(target, "target")
+    if draft is not None and _dtype_code(draft, "draft") != code:
+        _refuse("target and draft must have one type")
+    if workspace.numel() * workspace.element_size() < mk_tree_verify_workspace_bytes(B, n, V):
+        _refuse("the workspace is smaller than mk_tree_verify_workspace_bytes")
+    sh = mk_verify_shape(code, B, n, V, ts[0], ts[1], ds[0], ds[1])
+    with _on_device(target, draft, tokens, parents, n_nodes, u, r, temperature, draft_temperature, path, n_path,
+                    next_token, workspace):
+        _check(_lib.mk_tree_verify(
+            ctypes.byref(sh), target.data_ptr(), None if draft is None else draft.data_ptr(),
+            _index_ptr(tokens, (B, n), "tokens"), _index_ptr(parents, (B, n), "parents"),
+            _index_ptr(n_nodes, (B,), "n_nodes"), _index_ptr(u, (B, n), "u"), _index_ptr(r, (B,), "r"),
+            _index_ptr(temperature, (B,), "temperature"), _index_ptr(draft_temperature, (B,), "draft_temperature"),
+            _index_ptr(path, (B, n), "path"), _index_ptr(n_path, (B,), "n_path"),
+            _index_ptr(next_token, (B,), "next_token"), workspace.data_ptr(), _stream(stream)))
+
+
+def _cache(kv, lens):
+    """mk_cache_shape of a cache tensor [layers, 2, max_batch, n_kv_heads, max_seq, head_dim] and
+    lengths [B], B <= max_batch."""
+    if kv.dim() != 6 or kv.shape[1] != 2 or not kv.is_contiguous() or kv.element_size() != 2:
+        _refuse("the cache must be a contiguous 16-bit tensor [layers, 2, max_batch, n_kv_heads, max_seq, head_dim]")
+    L, _, mb, hkv, S, d = kv.shape
+    return mk_cache_shape(L, mb, lens.shape[0], hkv, S, d)
+
+
+def mk_cache_commit(kv, path, n_path, lens, new_lens, stream=None):
+    """Keep the accepted nodes' rows of a cache (``Megakernel.kv_view()``): row lens[b] +
+    path[b][j] moves to lens[b] + j.  path [B, n], n_path, lens, new_lens [B] int32."""
+    sh, B, n = _cache(kv, lens), lens.shape[0], path.shape[-1]
+    with _on_device(kv, path, n_path, lens, new_lens):
+        _check(_lib.mk_cache_commit(ctypes.byref(sh), kv.data_ptr(), _index_ptr(path, (B, n), "path"), n,
+                                    _index_ptr(n_path, (B,), "n_path"), _index_ptr(lens, (B,), "lens"),
+                                    _index_ptr(new_lens, (B,), "new_lens"), _stream(stream)))
+
+
+def mk_cache_reorder(kv, src, lens, new_lens, stream=None):
+    """Sequence b of a cache (``Megakernel.kv_view()``) takes the rows of sequence src[b].  src,
+    lens, new_lens [B] int32."""
+    sh, B = _cache(kv, lens), lens.shape[0]
+    with _on_device(kv, src, lens, new_lens):
+        _check(_lib.mk_cache_reorder(ctypes.byref(sh), kv.data_ptr(), _index_ptr(src, (B,), "src"),
+                                     _index_ptr(lens, (B,), "lens"), _index_ptr(new_lens, (B,), "new_lens"),
+                                     _stream(stream)))
 
 
 def mk_last_error(ctx=None) -> str:

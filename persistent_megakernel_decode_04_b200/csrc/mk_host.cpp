@@ -2116,6 +2116,72 @@ int mk_tree_attention_status(void* stream) {
   return MK_OK;
 }
 
+size_t mk_tree_verify_workspace_bytes(int B, int n, int vocab) {
+  if (B < 1 || n < 1 || n > MK_MAX_TREE_NODES || vocab < 1) return 0;
+  return tree_verify_workspace_bytes(B, n, vocab);
+}
+
+int mk_tree_verify(const mk_verify_shape* shape, const void* target, const void* draft, const int32_t* tokens,
+                   const int32_t* parents, const int32_t* n_nodes, const float* u, const float* r,
+                   const float* temperature, const float* draft_temperature, int32_t* path, int32_t* n_path,
+                   int32_t* next_token, void* workspace, void* stream) {
+  if (!shape || !target || !tokens || !parents || !u || !r || !path || !n_path || !next_token)
+    return fail(nullptr, MK_ERR_INVALID_ARG, "NULL operand");
+  const mk_verify_shape& s = *shape;
+  if (s.dtype != MK_FP32 && s.dtype != MK_BF16 && s.dtype != MK_FP16)
+    return fail(nullptr, MK_ERR_INVALID_ARG, "tree verify takes MK_FP32, MK_BF16 or MK_FP16 logits");
+  if (s.B < 1 || s.n < 1 || s.n > MK_MAX_TREE_NODES || s.vocab < 1 || s.vocab > (1 << 23))
+    return fail(nullptr, MK_ERR_INVALID_ARG, "bad B, n or vocab (at most 2^23)");
+  if ((int64_t)s.B * s.n > 65535) return fail(nullptr, MK_ERR_INVALID_ARG, "B * n must be at most 65535");
+  const int size = s.dtype == MK_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) % size)
+    return fail(nullptr, MK_ERR_INVALID_ARG, "logits must be aligned to their type");
+  if ((s.B > 1 && s.t_seq < 0) || (s.n > 1 && s.t_node < 0) || (draft && ((s.B > 1 && s.d_seq < 0) || (s.n > 1 && s.d_node < 0))))
+    return fail(nullptr, MK_ERR_INVALID_ARG, "negative strides");
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))
+    return fail(nullptr, MK_ERR_INVALID_ARG, "workspace must be a 16-byte aligned device pointer");
+  TreeVerify a = {s.dtype, s.B, s.n, s.vocab, target, draft, s.t_seq, s.t_node, s.d_seq, s.d_node, tokens, parents,
+                  n_nodes, u, r, temperature, draft_temperature, path, n_path, next_token};
+  std::string err;
+  const int rc = tree_verify(a, workspace, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(nullptr, rc, err);
+  return MK_OK;
+}
+
+static int check_cache(const mk_cache_shape* s, const void* cache, const int32_t* lens, const int32_t* new_lens) {
+  if (!s || !cache || !lens || !new_lens) return fail(nullptr, MK_ERR_INVALID_ARG, "NULL operand");
+  if (s->n_layers < 1 || s->B < 1 || s->B > s->max_batch || s->n_kv_heads < 1 || s->max_seq < 1 ||
+      (s->head_dim != 64 && s->head_dim != 128) || (int64_t)s->n_layers * s->n_kv_heads > (1 << 24) ||
+      s->B > 65535 || s->max_seq > (1 << 26))
+    return fail(nullptr, MK_ERR_INVALID_ARG, "bad n_layers, B, max_batch, n_kv_heads, max_seq or head_dim");
+  if (reinterpret_cast<uintptr_t>(cache) & 15) return fail(nullptr, MK_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
+  const uintptr_t a = reinterpret_cast<uintptr_t>(lens), c = reinterpret_cast<uintptr_t>(new_lens), size = 4u * s->B;
+  if (a < c + size && c < a + size) return fail(nullptr, MK_ERR_INVALID_ARG, "new_lens must not overlap lens");
+  return MK_OK;
+}
+
+int mk_cache_commit(const mk_cache_shape* shape, void* cache, const int32_t* path, int n, const int32_t* n_path,
+                    const int32_t* lens, int32_t* new_lens, void* stream) {
+  if (const int rc = check_cache(shape, cache, lens, new_lens)) return rc;
+  if (!path || !n_path) return fail(nullptr, MK_ERR_INVALID_ARG, "NULL operand");
+  if (n < 1 || n > MK_MAX_TREE_NODES) return fail(nullptr, MK_ERR_INVALID_ARG, "bad n");
+  std::string err;
+  const int rc = cache_commit(*shape, cache, path, n, n_path, lens, new_lens, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(nullptr, rc, err);
+  return MK_OK;
+}
+
+int mk_cache_reorder(const mk_cache_shape* shape, void* cache, const int32_t* src, const int32_t* lens,
+                     int32_t* new_lens, void* stream) {
+  if (const int rc = check_cache(shape, cache, lens, new_lens)) return rc;
+  if (!src) return fail(nullptr, MK_ERR_INVALID_ARG, "NULL operand");
+  if (shape->B > MK_MAX_BATCH) return fail(nullptr, MK_ERR_INVALID_ARG, "at most MK_MAX_BATCH sequences");
+  std::string err;
+  const int rc = cache_reorder(*shape, cache, src, lens, new_lens, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(nullptr, rc, err);
+  return MK_OK;
+}
+
 int mk_attention_noalloc_status(void* stream) {
   std::string err;
   const int rc = attention_noalloc_status(reinterpret_cast<cudaStream_t>(stream), &err);

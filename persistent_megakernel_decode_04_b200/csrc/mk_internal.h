@@ -228,6 +228,20 @@ int tree_attention(const mk_tree_shape& s, const void* q, const void* k, const v
                    const int32_t* parents, const int32_t* n_nodes, const int32_t* lens, float scale, int n_sms,
                    cudaStream_t stream, std::string* err);
 int tree_attention_status(cudaStream_t stream, std::string* err);
+struct TreeVerify {
+  int dtype, B, n, vocab;
+  const void *target, *draft;
+  int64_t t_seq, t_node, d_seq, d_node;
+  const int32_t *tokens, *parents, *n_nodes;
+  const float *u, *r, *temperature, *draft_temperature;
+  int32_t *path, *n_path, *next_token;
+};
+size_t tree_verify_workspace_bytes(int B, int n, int vocab);
+int tree_verify(const TreeVerify& a, void* workspace, cudaStream_t stream, std::string* err);
+int cache_commit(const mk_cache_shape& s, void* cache, const int32_t* path, int n, const int32_t* n_path,
+                 const int32_t* lens, int32_t* new_lens, cudaStream_t stream, std::string* err);
+int cache_reorder(const mk_cache_shape& s, void* cache, const int32_t* src, const int32_t* lens, int32_t* new_lens,
+                  cudaStream_t stream, std::string* err);
 
 // Prefill (mk_prefill.cu).
 struct PrefillParams {

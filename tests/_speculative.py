@@ -66,3 +66,55 @@ def attention_bound(o, a, v, dtype):
     h = torch.finfo(dtype).eps / 2
     tiny = 2.0 ** -32 * v.double().abs().amax() * v.shape[2] + 2.0 ** -25 if dtype == torch.float16 else 1e-30
     return h * (1 + h) * (o.abs() + a) + 2 * (2.0 ** -11 + 2.0 ** -13) * a + tiny
+
+
+def softmax_long(x, temperature):
+    """Softmax of x / temperature in extended precision; temperature 0: one-hot at the largest
+    value's lowest index; None where x is no distribution."""
+    x = x.astype(np.longdouble)
+    if np.isnan(x).any() or (x == np.inf).any() or (x == -np.inf).all():
+        return None
+    if temperature == 0:
+        return (np.arange(x.size) == int(np.argmax(x))).astype(np.longdouble)
+    e = np.exp((x - x.max()) / np.longdouble(temperature))
+    return e / e.sum()
+
+
+def verify_walk(target, draft, tokens, parents, n_nodes, u, r, temperature, draft_temperature):
+    """path, next token and the smallest relative distance of any decision to its border, for one
+    sequence (numpy arrays)."""
+    V = target.shape[1]
+    margin = np.inf
+    if n_nodes == 0:
+        return [], -1, margin
+    greedy = temperature == 0
+    word = np.arange(V)
+    path, cur = [0], 0
+    P = softmax_long(target[0], temperature)
+    for c in range(1, n_nodes):
+        if parents[c] != cur or P is None:
+            continue
+        x = int(tokens[c])
+        if greedy or draft is None:
+            q = (word == x).astype(np.longdouble)
+        else:
+            q = softmax_long(draft[cur], draft_temperature)
+        qx, px = (q[x], P[x]) if 0 <= x < V else (np.longdouble(draft is None or greedy), np.longdouble(0))
+        a = np.longdouble(0 if greedy else u[c]) * qx
+        if max(a, px) > 0:
+            margin = min(margin, abs(a - px) / max(a, px))
+        if a < px:
+            path.append(c)
+            cur, P = c, softmax_long(target[c], temperature)
+        elif not greedy:
+            rest = np.maximum(P - q, 0)
+            if rest.sum() > 0:
+                P = rest / rest.sum()
+    if P is None:
+        return path, -1, margin
+    cum = np.cumsum(P)
+    want = np.longdouble(r) * cum[-1]
+    at = int(np.nonzero((cum > want) & (P > 0))[0][0]) if not greedy else int(np.argmax(P))
+    if not greedy:
+        margin = min(margin, float(abs(cum - want)[P > 0].min()) * V)
+    return path, at, margin

@@ -437,7 +437,7 @@ typedef struct mk_verify_shape {
  *   count; next_token: int32 [B] (-1 where the last node's logits are no distribution: NaN,
  *   infinite, or only -inf; children of such a node are not accepted; -1 with n_path 0 for a
  *   sequence without nodes).
- * Sums that a draw depends on are formed in 64 bits.  workspace: device scratch of
+ * Requirements: vocab <= 2^20, B * n <= 65535.  Sums that a draw depends on are formed in 64 bits.  workspace: device scratch of
  * mk_tree_verify_workspace_bytes, 16-byte aligned, its contents do not matter; calls that share it
  * must not overlap (nor may replays of graphs that captured such calls).  Two launches. */
 size_t mk_tree_verify_workspace_bytes(int B, int n, int vocab);

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -126,13 +127,13 @@ _SIGS = {
     "mk_attention_noalloc_status": ([_vp], _i32),
     "mk_attention_set_wait_timeout_ns": ([_u64], _i32),
     "mk_attention_debug_drop_unit": ([_i32], _i32),
-    "mk_tree_attention": ([ctypes.POINTER(mk_tree_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp],
+    "mk_tree_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp],
                           _i32),
     "mk_tree_attention_status": ([_vp], _i32),
     "mk_tree_verify_workspace_bytes": ([_i32, _i32, _i32], _sz),
-    "mk_tree_verify": ([ctypes.POINTER(mk_verify_shape)] + [_vp] * 14, _i32),
-    "mk_cache_commit": ([ctypes.POINTER(mk_cache_shape), _vp, _vp, _i32, _vp, _vp, _vp, _vp], _i32),
-    "mk_cache_reorder": ([ctypes.POINTER(mk_cache_shape), _vp, _vp, _vp, _vp, _vp], _i32),
+    "mk_tree_verify": ([_vp] * 15, _i32),
+    "mk_cache_commit": ([_vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp], _i32),
+    "mk_cache_reorder": ([_vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "mk_last_error": ([_vp], ctypes.c_char_p),
     "mk_destroy": ([_vp], None),
 }
@@ -386,52 +387,52 @@ def mk_attention_debug_drop_unit(unit: int):
     _check(_lib.mk_attention_debug_drop_unit(int(unit)))
 
 
-# ---- speculative decoding: these take torch tensors and read sizes, strides and types off them
+# ---- speculative decoding: these take torch tensors and read sizes, strides and types off them.
+# A decoding loop makes these calls for kernels of a few microseconds, so the checks are kept
+# cheap: plain comparisons, and the shape structs packed instead of built field by field.
+
+_TREE_SHAPE = struct.Struct("7i4x12q")
+_VERIFY_SHAPE = struct.Struct("4i4q")
+_CACHE_SHAPE = struct.Struct("6i")
+_types = None  # (torch, {dtype: code}): torch is only imported by the calls that take tensors
+
+
+def _torch_types():
+    global _types
+    import torch
+    # int16 holds bf16 bits (Megakernel.kv_view)
+    _types = (torch, {torch.bfloat16: MK_BF16, torch.int16: MK_BF16, torch.float16: MK_FP16, torch.float32: MK_FP32})
+    return _types
+
 
 def _refuse(msg):
     raise MkError(MK_ERR_INVALID_ARG, msg)
 
 
-def _dtype_code(t, what):
-    """MK_BF16 / MK_FP16 / MK_FP32 of a tensor; int16 holds bf16 bits (Megakernel.kv_view)."""
-    name = str(t.dtype)
-    code = {"torch.bfloat16": MK_BF16, "torch.int16": MK_BF16, "torch.float16": MK_FP16,
-            "torch.float32": MK_FP32}.get(name)
-    if code is None:
-        _refuse(f"{what}: {name} is not supported")
-    return code
-
-
-def _index_ptr(t, shape, what):
-    """data_ptr of a contiguous tensor of `shape` (None: NULL); indices are int32, the rest fp32."""
+def _index(t, shape, dtype, what):
+    """data_ptr of a contiguous tensor of `shape` and `dtype` (None: NULL)."""
     if t is None:
         return None
-    want = "torch.float32" if what in ("u", "r", "temperature", "draft_temperature") else "torch.int32"
-    if tuple(t.shape) != shape or str(t.dtype) != want or not t.is_contiguous():
-        _refuse(f"{what} must be a contiguous {want} tensor of shape {shape}")
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
-class _on_device:
-    """The tensors' device made current for the call (they all have to be on it)."""
-
-    def __init__(self, first, *others):
-        dev = first.device
-        for t in others:
-            if t is not None and t.device != dev:
-                _refuse(f"tensors on {dev} and {t.device}")
-        if dev.type != "cuda":
-            _refuse(f"tensors must be on a CUDA device, not {dev}")
-        import torch
-        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _call(torch, f, tensors, *args):
+    """f(*args) with the tensors' device current; they all have to be on it."""
+    dev = tensors[0].get_device()
+    if dev < 0:
+        _refuse("tensors must be on a CUDA device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse(f"tensors on {tensors[0].device} and {t.device}")
+    if torch.cuda.current_device() == dev:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args)
+    if rc:
+        _check(rc)
 
 
 def mk_tree_attention(q, k, v, o, parents, n_nodes, lens, scale: float, stream=None):
@@ -439,24 +440,27 @@ def mk_tree_attention(q, k, v, o, parents, n_nodes, lens, scale: float, stream=N
     n_kv_heads, max_seq, head_dim] (e.g. ``kv_view()[layer, 0]`` and ``[layer, 1]``); bf16 or
     fp16, any strides with a contiguous last axis; parents [B, n], lens [B] and n_nodes [B] (or
     None) int32."""
+    torch, codes = _types or _torch_types()
     if q.dim() != 4 or k.dim() != 4 or o.shape != q.shape or v.shape != k.shape:
         _refuse("q and o must be [B, n, n_q_heads, head_dim], k and v [B, n_kv_heads, max_seq, head_dim]")
     B, n, hq, d = q.shape
-    if k.shape[0] != B or k.shape[3] != d:
+    kB, hkv, S, kd = k.shape
+    if kB != B or kd != d:
         _refuse("q and k differ in batch or head_dim")
-    code = _dtype_code(q, "q")
-    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
-    for t, what, st in ((q, "q", qs), (k, "k", ks), (v, "v", vs), (o, "o", os_)):
-        if _dtype_code(t, what) != code:
-            _refuse("q, k, v and o must have one type")
-        if st[3] != 1:
-            _refuse(f"{what}: the last axis must be contiguous")
-    sh = mk_tree_shape(code, B, n, hq, k.shape[1], d, k.shape[2], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
-                       vs[0], vs[1], vs[2], os_[0], os_[1], os_[2])
-    with _on_device(q, k, v, o, parents, n_nodes, lens):
-        _check(_lib.mk_tree_attention(ctypes.byref(sh), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                      _index_ptr(parents, (B, n), "parents"), _index_ptr(n_nodes, (B,), "n_nodes"),
-                                      _index_ptr(lens, (B,), "lens"), scale, _stream(stream)))
+    code = codes.get(q.dtype)
+    if code is None or not (code == codes.get(k.dtype) == codes.get(v.dtype) == codes.get(o.dtype)):
+        _refuse("q, k, v and o must have one type: bfloat16 (or its bits as int16) or float16")
+    q0, q1, q2, q3 = q.stride()
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
+    o0, o1, o2, o3 = o.stride()
+    if not q3 == k3 == v3 == o3 == 1:
+        _refuse("the last axis of q, k, v and o must be contiguous")
+    i32 = torch.int32
+    _call(torch, _lib.mk_tree_attention, (q, k, v, o, parents, lens, n_nodes),
+          _TREE_SHAPE.pack(code, B, n, hq, hkv, d, S, q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2),
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _index(parents, (B, n), i32, "parents"),
+          _index(n_nodes, (B,), i32, "n_nodes"), _index(lens, (B,), i32, "lens"), scale, _stream(stream))
 
 
 def mk_tree_attention_status(stream=None) -> int:
@@ -475,57 +479,57 @@ def mk_tree_verify(target, draft, tokens, parents, n_nodes, u, r, temperature, d
     logits [B, n, vocab] in fp32, bf16 or fp16 with a contiguous last axis; tokens, parents, path
     [B, n], n_nodes (or None), n_path, next_token [B] int32; u [B, n], r, temperature,
     draft_temperature [B] (the last two or None) fp32."""
-    if target.dim() != 3 or (draft is not None and draft.shape != target.shape):
-        _refuse("target and draft must be [B, n, vocab]")
+    torch, codes = _types or _torch_types()
+    if target.dim() != 3 or (draft is not None and (draft.shape != target.shape or draft.dtype is not target.dtype)):
+        _refuse("target and draft must be [B, n, vocab], of one type")
     B, n, V = target.shape
-    ts = target.stride()
-    ds = draft.stride() if draft is not None else ts
-    if ts[2] != 1 or ds[2] != 1:
-        _refuse("the logits' last axis must be contiguous")
-    code = _dtype_code(target, "target")
-    if draft is not None and _dtype_code(draft, "draft") != code:
-        _refuse("target and draft must have one type")
-    if workspace.numel() * workspace.element_size() < mk_tree_verify_workspace_bytes(B, n, V):
+    t0, t1, t2 = target.stride()
+    d0, d1, d2 = draft.stride() if draft is not None else (0, 0, 1)
+    code = codes.get(target.dtype)
+    if code is None or target.dtype is torch.int16 or t2 != 1 or d2 != 1:
+        _refuse("the logits must be float32, bfloat16 or float16 with a contiguous last axis")
+    if workspace.nbytes < _lib.mk_tree_verify_workspace_bytes(B, n, V):
         _refuse("the workspace is smaller than mk_tree_verify_workspace_bytes")
-    sh = mk_verify_shape(code, B, n, V, ts[0], ts[1], ds[0], ds[1])
-    with _on_device(target, draft, tokens, parents, n_nodes, u, r, temperature, draft_temperature, path, n_path,
-                    next_token, workspace):
-        _check(_lib.mk_tree_verify(
-            ctypes.byref(sh), target.data_ptr(), None if draft is None else draft.data_ptr(),
-            _index_ptr(tokens, (B, n), "tokens"), _index_ptr(parents, (B, n), "parents"),
-            _index_ptr(n_nodes, (B,), "n_nodes"), _index_ptr(u, (B, n), "u"), _index_ptr(r, (B,), "r"),
-            _index_ptr(temperature, (B,), "temperature"), _index_ptr(draft_temperature, (B,), "draft_temperature"),
-            _index_ptr(path, (B, n), "path"), _index_ptr(n_path, (B,), "n_path"),
-            _index_ptr(next_token, (B,), "next_token"), workspace.data_ptr(), _stream(stream)))
+    i32, f32, one, two = torch.int32, torch.float32, (B,), (B, n)
+    _call(torch, _lib.mk_tree_verify,
+          (target, tokens, parents, u, r, path, n_path, next_token, workspace, draft, n_nodes, temperature,
+           draft_temperature),
+          _VERIFY_SHAPE.pack(code, B, n, V, t0, t1, d0, d1), target.data_ptr(),
+          None if draft is None else draft.data_ptr(), _index(tokens, two, i32, "tokens"),
+          _index(parents, two, i32, "parents"), _index(n_nodes, one, i32, "n_nodes"), _index(u, two, f32, "u"),
+          _index(r, one, f32, "r"), _index(temperature, one, f32, "temperature"),
+          _index(draft_temperature, one, f32, "draft_temperature"), _index(path, two, i32, "path"),
+          _index(n_path, one, i32, "n_path"), _index(next_token, one, i32, "next_token"), workspace.data_ptr(),
+          _stream(stream))
 
 
-def _cache(kv, lens):
-    """mk_cache_shape of a cache tensor [layers, 2, max_batch, n_kv_heads, max_seq, head_dim] and
-    lengths [B], B <= max_batch."""
-    if kv.dim() != 6 or kv.shape[1] != 2 or not kv.is_contiguous() or kv.element_size() != 2:
+def _cache(kv, B):
+    """Packed mk_cache_shape of a cache tensor [layers, 2, max_batch, n_kv_heads, max_seq,
+    head_dim] whose first B sequences are meant."""
+    if kv.dim() != 6 or not kv.is_contiguous() or kv.element_size() != 2 or kv.shape[1] != 2:
         _refuse("the cache must be a contiguous 16-bit tensor [layers, 2, max_batch, n_kv_heads, max_seq, head_dim]")
     L, _, mb, hkv, S, d = kv.shape
-    return mk_cache_shape(L, mb, lens.shape[0], hkv, S, d)
+    return _CACHE_SHAPE.pack(L, mb, B, hkv, S, d)
 
 
 def mk_cache_commit(kv, path, n_path, lens, new_lens, stream=None):
     """Keep the accepted nodes' rows of a cache (``Megakernel.kv_view()``): row lens[b] +
     path[b][j] moves to lens[b] + j.  path [B, n], n_path, lens, new_lens [B] int32."""
-    sh, B, n = _cache(kv, lens), lens.shape[0], path.shape[-1]
-    with _on_device(kv, path, n_path, lens, new_lens):
-        _check(_lib.mk_cache_commit(ctypes.byref(sh), kv.data_ptr(), _index_ptr(path, (B, n), "path"), n,
-                                    _index_ptr(n_path, (B,), "n_path"), _index_ptr(lens, (B,), "lens"),
-                                    _index_ptr(new_lens, (B,), "new_lens"), _stream(stream)))
+    torch, _ = _types or _torch_types()
+    B, n, i32 = lens.shape[0], path.shape[-1], torch.int32
+    _call(torch, _lib.mk_cache_commit, (kv, path, n_path, lens, new_lens), _cache(kv, B), kv.data_ptr(),
+          _index(path, (B, n), i32, "path"), n, _index(n_path, (B,), i32, "n_path"), _index(lens, (B,), i32, "lens"),
+          _index(new_lens, (B,), i32, "new_lens"), _stream(stream))
 
 
 def mk_cache_reorder(kv, src, lens, new_lens, stream=None):
     """Sequence b of a cache (``Megakernel.kv_view()``) takes the rows of sequence src[b].  src,
     lens, new_lens [B] int32."""
-    sh, B = _cache(kv, lens), lens.shape[0]
-    with _on_device(kv, src, lens, new_lens):
-        _check(_lib.mk_cache_reorder(ctypes.byref(sh), kv.data_ptr(), _index_ptr(src, (B,), "src"),
-                                     _index_ptr(lens, (B,), "lens"), _index_ptr(new_lens, (B,), "new_lens"),
-                                     _stream(stream)))
+    torch, _ = _types or _torch_types()
+    B, i32 = lens.shape[0], torch.int32
+    _call(torch, _lib.mk_cache_reorder, (kv, src, lens, new_lens), _cache(kv, B), kv.data_ptr(),
+          _index(src, (B,), i32, "src"), _index(lens, (B,), i32, "lens"), _index(new_lens, (B,), i32, "new_lens"),
+          _stream(stream))
 
 
 def mk_last_error(ctx=None) -> str:

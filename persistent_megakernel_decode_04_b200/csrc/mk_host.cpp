@@ -2130,8 +2130,8 @@ int mk_tree_verify(const mk_verify_shape* shape, const void* target, const void*
   const mk_verify_shape& s = *shape;
   if (s.dtype != MK_FP32 && s.dtype != MK_BF16 && s.dtype != MK_FP16)
     return fail(nullptr, MK_ERR_INVALID_ARG, "tree verify takes MK_FP32, MK_BF16 or MK_FP16 logits");
-  if (s.B < 1 || s.n < 1 || s.n > MK_MAX_TREE_NODES || s.vocab < 1 || s.vocab > (1 << 23))
-    return fail(nullptr, MK_ERR_INVALID_ARG, "bad B, n or vocab (at most 2^23)");
+  if (s.B < 1 || s.n < 1 || s.n > MK_MAX_TREE_NODES || s.vocab < 1 || s.vocab > (1 << 20))
+    return fail(nullptr, MK_ERR_INVALID_ARG, "bad B, n or vocab (at most 2^20)");
   if ((int64_t)s.B * s.n > 65535) return fail(nullptr, MK_ERR_INVALID_ARG, "B * n must be at most 65535");
   const int size = s.dtype == MK_FP32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) % size)

@@ -25,6 +25,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mk_internal.h"
 #include "mk_ptx.cuh"
@@ -38,8 +39,10 @@ constexpr int kChunk = 8192;        // elements of a row per block of row_stats
 constexpr int kThreads = 512;       // walk
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kPass = kThreads * 4;  // elements of a block's pass step: 4 per thread
+constexpr int kPer = 8;              // elements per thread and step of a pass
+constexpr int kPass = kThreads * kPer;
 constexpr float kClose = 1e-5f;
+constexpr int kMaxDyn = 192 * 1024;  // walk: dynamic shared memory
 
 struct Stat {  // of one row's chunk
   float m, s;
@@ -54,6 +57,7 @@ struct Params {
   int32_t *path, *n_path, *next_token;
   Stat* stats;  // [target | draft][B][n][chunks]
   int B, n, V, chunks;
+  int keep;  // walk: a pass keeps its values in shared memory: 0 no, 1 of the target, 2 and of the draft
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -64,6 +68,46 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// -infinity; the largest of a 16-byte piece (NaN left out); its values.
+template <typename T>
+__device__ __forceinline__ T lowest();
+template <>
+__device__ __forceinline__ float lowest<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 lowest<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff80); }
+template <>
+__device__ __forceinline__ __half lowest<__half>() { return __ushort_as_half(0xfc00); }
+
+template <typename T>
+__device__ __forceinline__ void floats_of(const uint4& v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      x[k] = __uint_as_float(w[k]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      x[2 * k] = bf16lo(w[k]), x[2 * k + 1] = bf16hi(w[k]);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      x[2 * k] = f.x, x[2 * k + 1] = f.y;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ float max_of(const uint4& v) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    const __half2* h = reinterpret_cast<const __half2*>(&v);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
 }
 
 __device__ __forceinline__ int in_use(const Params& P, int b) {
@@ -93,56 +137,69 @@ __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
                        : static_cast<const T*>(P.target) + b * P.t_seq + i * P.t_node;
   const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));  // elements since the last border
   const int j0 = blockIdx.x * kChunk - lead;
-  float x[kSteps][kVec];
+  uint4 raw[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int j = j0 + (s * kStatThreads + (int)threadIdx.x) * kVec;
     if (j >= 0 && j + kVec <= P.V) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + j);
-      const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) x[s][k] = to_f(e[k]);
+      raw[s] = *reinterpret_cast<const uint4*>(row + j);
     } else {
+      T* e = reinterpret_cast<T*>(&raw[s]);
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) x[s][k] = j + k >= 0 && j + k < P.V ? to_f(row[j + k]) : -INFINITY;
+      for (int k = 0; k < kVec; ++k) e[k] = j + k >= 0 && j + k < P.V ? row[j + k] : lowest<T>();
     }
   }
-  float m = -INFINITY;
+  // NaN takes no part in the maximum; it comes out of the sum
+  float own = -INFINITY;
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) m = fmaxf(m, x[s][k]);
+  for (int s = 0; s < kSteps; ++s) own = fmaxf(own, max_of<T>(raw[s]));
+  float m = own;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ float sm[kStatThreads / 32], ss[kStatThreads / 32];
-  __shared__ int si[kStatThreads / 32];
+  __shared__ int si;
 #pragma unroll
   for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   if (lane == 0) sm[warp] = m;
+  if (threadIdx.x == 0) si = 0x7fffffff;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kStatThreads / 32; ++k) m = fmaxf(m, sm[k]);
   const float base = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-  int idx = 0x7fffffff;
+  const uint64_t nb = pack2(-base, -base), cc = pack2(c, c);
+  uint64_t acc = 0;  // two sums
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    const int j = j0 + (s * kStatThreads + (int)threadIdx.x) * kVec;
+    float x[kVec];
+    floats_of<T>(raw[s], x);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      sum += ex2((x[s][k] - base) * c);  // at temperature 0 c is infinite: the sum is not used
-      if (x[s][k] == m && j + k >= 0 && j + k < P.V) idx = min(idx, j + k);
+    for (int k = 0; k < kVec; k += 2) {  // exp2((x - base) c); at temperature 0 the sum is not used
+      uint64_t y = pack2(x[k], x[k + 1]);
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(nb));
+      asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(cc));
+      const float2 e = unpack2(y);
+      y = pack2(ex2(e.x), ex2(e.y));
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(y));
     }
   }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    idx = min(idx, __shfl_xor_sync(0xffffffffu, idx, off));
+  float sum = unpack2(acc).x + unpack2(acc).y;
+  if (own == m) {  // few threads: the lowest place of the maximum
+    int idx = 0x7fffffff;
+#pragma unroll 1
+    for (int s = 0; s < kSteps; ++s) {
+      const int j = j0 + (s * kStatThreads + (int)threadIdx.x) * kVec;
+      for (int k = 0; k < kVec; ++k)
+        if (j + k >= 0 && j + k < P.V && to_f(row[j + k]) == m) idx = min(idx, j + k);
+    }
+    atomicMin(&si, idx);
   }
-  if (lane == 0) ss[warp] = sum, si[warp] = idx;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) ss[warp] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int k = 1; k < kStatThreads / 32; ++k) sum += ss[k], idx = min(idx, si[k]);
-    P.stats[((int64_t)(draft * P.B + b) * P.n + i) * P.chunks + blockIdx.x] = Stat{m, sum, idx, 0};
+#pragma unroll
+    for (int k = 1; k < kStatThreads / 32; ++k) sum += ss[k];
+    P.stats[((int64_t)(draft * P.B + b) * P.n + i) * P.chunks + blockIdx.x] = Stat{m, sum, si, 0};
   }
 }
 
@@ -160,42 +217,51 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 2^y for y <= 0 by a table of 2^(k / 256) and a cubic in the remainder (|r| <= 2^-9: the next
-// term of the series is below 1.4e-13).  The method is P. T. P. Tang's, "Table-driven
-// implementation of the exponential function in IEEE floating-point arithmetic", 1989.
-__device__ __forceinline__ double exp2_table(double y, const double* table) {
-  constexpr double kMagic = 6755399441055744.0 / 256;  // 1.5 * 2^52 / 256: the sum's low bits are round(256 y)
-  if (!(y > -1000.0)) return y != y ? y : 0.0;
+// 2^y for -1000 <= y <= 0 by a table of 2^(k / 16) and the series of 2^r in the remainder (|r| <=
+// 1/32; the term behind the fifth is below 1.5e-13).  The method is P. T. P. Tang's, "Table-driven
+// implementation of the exponential function in IEEE floating-point arithmetic", 1989.  The table
+// is kept 16 times, a copy for every other lane, so that lookups meet no bank conflicts (with 256
+// entries once they took half of a pass).  `low`: y is below -1000, the value 0 (told apart in fp32,
+// without a branch: several run side by side).
+constexpr int kTable = 16, kCopies = 16;
+__device__ __forceinline__ double exp2_table(double y, bool low, const double* table) {
+  constexpr double kMagic = 6755399441055744.0 / kTable;  // 1.5 * 2^52 / 16: the sum's low bits are round(16 y)
   const double t = y + kMagic;
   const int k = __double2loint(t);
   const double r = y - (t - kMagic);
-  constexpr double c1 = 0.69314718055994530942, c2 = c1 * c1 / 2, c3 = c1 * c1 * c1 / 6;
-  double e = table[k & 255];
-  e = __hiloint2double(__double2hiint(e) + ((k >> 8) << 20), __double2loint(e));
-  return fma(e, r * fma(r, fma(r, c3, c2), c1), e);
+  constexpr double c1 = 0.69314718055994530942, c2 = c1 * c1 / 2, c3 = c2 * c1 / 3, c4 = c3 * c1 / 4, c5 = c4 * c1 / 5;
+  double e = table[(k & (kTable - 1)) * kCopies + (threadIdx.x & (kCopies - 1))];
+  e = __hiloint2double(__double2hiint(e) + ((k >> 4) << 20), __double2loint(e));
+  e = fma(e, r * fma(r, fma(r, fma(r, fma(r, c5, c4), c3), c2), c1), e);
+  return low ? 0.0 : e;
 }
 
 enum Op { OP_DONE, OP_SUMS, OP_REST, OP_AGAIN };
 
 struct Ctl {
-  double table[256];
-  double sums[2][3][kMaxCluster];  // a pass's partial sums of every block, by turns
-  double warp_sum[kWarps];
-  double total[3];
-  double ZP, ZQ, Z[kMaxNodes];    // sums of a node's exponentials; of its rests so far
-  float m[2][kMaxNodes], z[2][kMaxNodes];
-  int idx[kMaxNodes];
-  int16_t parent[kMaxNodes], gone[kMaxNodes];
-  int32_t token[kMaxNodes];
-  float u[kMaxNodes];
+  double table[kTable * kCopies];
+  double sums[2][2][kMaxCluster];  // a pass's partial sums (P, q) of every block, by turns
+  double warp_sum[2][kWarps];
+  double total;                    // of the last pass
+  double iP, iQ, iZ[kMaxNodes];    // 1 / sum of a node's exponentials; 1 / sum of its rests so far
   double p[kMaxNodes], q[kMaxNodes];  // exponentials of a child's token in its parent's rows
-  int op, cur, rounds, n_gone, found;
+  double inv[kMaxNodes];              // 1 / sum of a node's exponentials by the fp32 statistics
+  float m[2][kMaxNodes], z[2][kMaxNodes], u[kMaxNodes], logit[2][kMaxNodes];
+  int idx[kMaxNodes];
+  int32_t token[kMaxNodes], gone[kMaxNodes];  // of a child; of the current node's rejected children
+  int16_t parent[kMaxNodes];
+  uint8_t first[kMaxNodes];        // a child's answer when it is the first one asked: 0, 1, 2 (too close)
+  uint8_t again[kMaxNodes];        // a child whose token an earlier sibling had, or outside the vocabulary
+  int op, cur, rounds, n_gone;
+  int kept;  // rejections that the kept values stand for (0: the exponentials), -1: none are kept
 };
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   __shared__ Ctl S;
-  extern __shared__ double piece[];  // sums of 128 elements each, in order: this block's slice of a row
+  // this block's slice of a row: the last pass's values of it (element k of thread t in step s at
+  // (s kPer + k) kThreads + t), the draft's exponentials alike, and sums of 32 kPer elements each
+  extern __shared__ double dyn[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t C, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
@@ -206,24 +272,32 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   const double kLog2e = 1.44269504088896340736;
   const double tc = kLog2e / (double)temp;
   const double dc = sampled ? kLog2e / (double)(P.draft_temperature ? P.draft_temperature[b] : 1.f) : 0.0;
+  const float tcf = (float)tc, dcf = (float)dc;
   const T* target = static_cast<const T*>(P.target) + b * P.t_seq;
   const T* draft = static_cast<const T*>(P.draft) + (sampled ? b * P.d_seq : 0);
 
-  for (int i = tid; i < nn; i += kThreads) {
-    S.parent[i] = (int16_t)max(-1, min(P.parents[(int64_t)b * n + i], n));
-    S.token[i] = P.tokens[(int64_t)b * n + i];
-    S.u[i] = greedy ? 0.f : P.u[(int64_t)b * n + i];
+  // the tree, and the logits of its tokens (a thread per node: n <= kThreads)
+  if (tid < nn) {
+    const int par = max(-1, min(P.parents[(int64_t)b * n + tid], n)), x = P.tokens[(int64_t)b * n + tid];
+    const bool asked = par >= 0 && par < tid && x >= 0 && x < V && !greedy;
+    S.parent[tid] = (int16_t)par;
+    S.token[tid] = x;
+    S.u[tid] = greedy ? 0.f : P.u[(int64_t)b * n + tid];
+    S.logit[0][tid] = asked ? to_f(target[par * P.t_node + x]) : -INFINITY;
+    S.logit[1][tid] = asked && sampled ? to_f(draft[par * P.d_node + x]) : -INFINITY;
   }
-  if (tid < 256 && !greedy) S.table[tid] = exp2(tid / 256.0);
+  if (tid < kTable * kCopies && !greedy) S.table[tid] = exp2(tid / kCopies / (double)kTable);
   cluster_sync();  // also: every block of the cluster has started
   asm volatile("griddepcontrol.wait;" ::: "memory");  // row_stats is done
   // a row's statistics from its chunks, a warp per row
+#pragma unroll 1
   for (int x = warp; x < nn * (sampled ? 2 : 1); x += kWarps) {
     const int d = x >= nn, i = d ? x - nn : x;
     const Stat* st = P.stats + ((int64_t)(d * P.B + b) * n + i) * P.chunks;
     float m = -INFINITY, z = 0.f;
     int idx = 0x7fffffff;
-    const float c = (float)(d ? dc : tc);
+    const float c = d ? dcf : tcf;
+#pragma unroll 1
     for (int k = lane; k < P.chunks; k += 32) {
       const Stat s = st[k];
       if (s.m > m) idx = s.idx;  // chunks in order: an equal maximum keeps the lower index
@@ -231,126 +305,137 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       z = z * ex2((m - base) * c) + s.s * ex2((s.m - base) * c);
       m = top;
     }
+    float top = m;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, off), z2 = __shfl_xor_sync(0xffffffffu, z, off);
-      const int i2 = __shfl_xor_sync(0xffffffffu, idx, off);
-      const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
-      idx = m == m2 ? min(idx, i2) : m > m2 ? idx : i2;
-      z = z * ex2((m - base) * c) + z2 * ex2((m2 - base) * c);
-      m = top;
-    }
+    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    z *= ex2((m - (top == -INFINITY ? 0.f : top)) * c);
+    idx = m == top ? idx : 0x7fffffff;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+    idx = __reduce_min_sync(0xffffffffu, idx);
     if (lane == 0) {
-      S.m[d][i] = m, S.z[d][i] = z;
+      S.m[d][i] = top, S.z[d][i] = z;
       if (!d) S.idx[i] = idx;
     }
   }
   __syncthreads();
-  if (!greedy)
-    for (int c = tid; c < nn; c += kThreads) {
-      const int par = S.parent[c], x = S.token[c];
-      double p = 0.0, q = 0.0;
-      if (par >= 0 && par < c && x >= 0 && x < V) {
-        p = exp2_table(((double)to_f(target[par * P.t_node + x]) - (double)S.m[0][par]) * tc, S.table);
-        if (sampled) q = exp2_table(((double)to_f(draft[par * P.d_node + x]) - (double)S.m[1][par]) * dc, S.table);
-      }
-      S.p[c] = p, S.q[c] = q;
+  if (tid < nn && !greedy) {
+    const int par = S.parent[tid];
+    const float lt = S.logit[0][tid], ld = S.logit[1][tid];
+    double p = 0.0, q = 0.0;
+    if (lt != -INFINITY) {  // (a NaN stays)
+      const float mt = S.m[0][par];
+      p = exp2_table(fma((double)lt, tc, -((double)mt * tc)), (lt - mt) * tcf <= -1000.f, S.table);
     }
+    if (sampled && ld != -INFINITY) {
+      const float md = S.m[1][par];
+      q = exp2_table(fma((double)ld, dc, -((double)md * dc)), (ld - md) * dcf <= -1000.f, S.table);
+    }
+    S.p[tid] = p, S.q[tid] = q;
+    S.inv[tid] = 1.0 / (double)S.z[0][tid];
+    if (par >= 0 && par < tid) {
+      // u q / ZQ < p / ZP without divisions
+      const double a = (double)S.u[tid] * (sampled ? q : 1.0) * (double)S.z[0][par];
+      const double e = p * (sampled ? (double)S.z[1][par] : 1.0), top = fmax(a, e);
+      S.first[tid] = fabs(a - e) <= (double)kClose * top && top > 0.0 ? 2 : a < e;
+    }
+    const int x = S.token[tid];
+    bool again = x < 0 || x >= V;
+    if (!sampled)
+      for (int k = par + 1; k < tid; ++k) again |= S.parent[k] == par && S.token[k] == x;
+    S.again[tid] = again;
+  }
   __syncthreads();
 
   // Thread 0 of every block walks; what it decides follows from the same numbers in each.
   int32_t* path = P.path + (int64_t)b * n;
   int cur = 0, depth = nn > 0 ? 1 : 0, c = 1;  // thread 0's
-  bool exact = false;                          // ZP, ZQ are the current node's
+  bool exact = false;                          // iP, iQ are the current node's
   bool summed = false;                         // `piece` holds the current P
-  if (tid == 0) {
-    S.rounds = S.n_gone = 0;
-    S.found = -1;
-  }
+  double left = 1.0;                           // without draft: what of P is not gone
+  if (tid == 0) S.rounds = S.n_gone = 0, S.kept = -1;
   int turn = 0;
-  const int slice = (((V + (int)C - 1) / (int)C) + 3) & ~3;  // elements per block
-  const int lo = min(V, (int)rank * slice), hi = min(V, lo + slice);
+  const int slice = (((V + 3 + (int)C - 1) / (int)C) + 3) & ~3;  // elements per block
+  const int room = (slice + kPass - 1) / kPass * kPass;
+  double* const kept_v = dyn + tid;
+  double* const kept_q = kept_v + room;
+  double* const piece = dyn + P.keep * room;
   for (;;) {
     if (tid == 0) {
       int op = OP_DONE;
+      int rounds = S.rounds, n_gone = S.n_gone;
       for (; c < nn; ++c) {
         if (S.parent[c] != cur) continue;
-        const int x = S.token[c];
+        bool take;
         if (greedy) {
+          const int x = S.token[c];
           if (x < 0 || x != S.idx[cur]) continue;
-        } else {
-          const double ZP = exact ? S.ZP : (double)S.z[0][cur], ZQ = sampled ? (exact ? S.ZQ : (double)S.z[1][cur]) : 1.0;
-          double p = S.p[c] / ZP, q = sampled ? S.q[c] / ZQ : 1.0, left = 1.0;
-          if (sampled) {
-            for (int k = 0; k < S.rounds; ++k) p = fmax(p - q, 0.0) / S.Z[k];
-          } else {
-            for (int k = 0; k < S.n_gone; ++k) {
-              left -= S.p[S.gone[k]] / ZP;
-              if (S.token[S.gone[k]] == x) p = 0.0;
-            }
-            p /= left;
-          }
-          const double a = (double)S.u[c] * q;
-          // (what is left of P is known to kClose / left)
-          if (!exact && (left < 0.125 || (fabs(a - p) <= kClose / left * fmax(a, p) && fmax(a, p) > 0.0))) {
+          take = true;
+        } else if (!exact && n_gone == 0) {
+          if (S.first[c] == 2) {
             op = OP_SUMS;  // too close for fp32 statistics: come back with exact ones
             break;
           }
-          if (!(a < p)) {
-            // rejected: what is left of P
-            if (sampled) {
-              op = exact ? OP_REST : OP_SUMS;
+          take = S.first[c];
+        } else {
+          const double iP = exact ? S.iP : S.inv[cur];
+          double p = S.p[c] * iP, a = (double)S.u[c];
+          if (sampled) {
+            const double q = S.q[c] * S.iQ;
+            for (int k = 0; k < rounds; ++k) p = fmax(p - q, 0.0) * S.iZ[k];
+            a *= q;
+          } else {
+            if (S.again[c]) p = 0.0;
+            a *= left;
+            // (fp32 statistics know what is left to kClose)
+            if (!exact && (left < 0.125 || fabs(a - p) * left <= (double)kClose * fmax(a, p))) {
+              op = OP_SUMS;
               break;
             }
-            bool known = x < 0 || x >= V;
-            for (int k = 0; k < S.n_gone; ++k) known |= S.token[S.gone[k]] == x;
-            if (!known) S.gone[S.n_gone++] = (int16_t)c, summed = false;
-            continue;
           }
+          take = a < p;
         }
-        if (rank == 0) path[depth] = c;
-        ++depth;
-        cur = c;
-        exact = summed = false;
-        S.rounds = S.n_gone = 0;
+        if (take) {
+          if (rank == 0) path[depth] = c;
+          ++depth;
+          cur = c;
+          exact = summed = false;
+          rounds = n_gone = 0;
+          left = 1.0;
+        } else if (sampled) {
+          op = exact ? OP_REST : OP_SUMS;  // rejected: what is left of P
+          break;
+        } else if (!S.again[c]) {
+          S.gone[n_gone++] = c;
+          left -= S.p[c] * (exact ? S.iP : S.inv[cur]);
+          summed = false;
+        }
       }
-      if (op == OP_DONE && !greedy && nn > 0 && !summed) op = S.rounds > 0 ? OP_AGAIN : OP_SUMS;
+      if (op == OP_DONE && !greedy && nn > 0 && !summed) op = rounds > 0 ? OP_AGAIN : OP_SUMS;
+      S.rounds = rounds, S.n_gone = n_gone;
       S.op = op;
       S.cur = cur;
     }
     __syncthreads();
     const int op = S.op;
     if (op == OP_DONE) break;
-    // ---- a pass over the current node's rows: this block's slice, 4 elements per thread and step.
+    // ---- a pass over the current node's rows: this block's slice, kPer elements per thread and step.
     // OP_SUMS: sums of the exponentials (without the tokens that are gone: also what is drawn
     // from when nothing was rejected).  OP_REST: the sum of the rest after one more rejection;
     // OP_AGAIN: after the rejections so far (the last OP_REST left nothing, and P stayed).
     const int node = S.cur;
     const T* tp = target + node * P.t_node;
     const T* dp = draft + (sampled ? node * P.d_node : 0);
-    const double mp = (double)S.m[0][node] * tc, mq = sampled ? (double)S.m[1][node] * dc : 0.0;
+    // slices and steps are counted from the last 4-element border before the target's row
+    const int lead = (int)((reinterpret_cast<uintptr_t>(tp) / sizeof(T)) & 3);
+    const bool d_vec = ((reinterpret_cast<uintptr_t>(dp) / sizeof(T)) & 3) == (uintptr_t)lead;
+    const int lo = (int)rank * slice - lead, hi = min(V, lo + slice);
+    const float mtf = S.m[0][node], mdf = S.m[1][node];
+    const double mp = -((double)mtf * tc), mq = -((double)mdf * dc);
     const int rounds = op == OP_SUMS ? 0 : S.rounds + (op == OP_REST), n_gone = S.n_gone;
-    const bool wants_q = sampled && (rounds > 0 || op == OP_SUMS);
-    const double iP = 1.0 / S.ZP, iQ = 1.0 / S.ZQ;
-    // the current P (op: SUMS unscaled, else after `rounds` rejections; the last one not yet scaled)
-    auto value = [&](int j, float tl, float dl, double& q) {
-      double v = exp2_table(fma((double)tl, tc, -mp), S.table);
-      if (wants_q) q = exp2_table(fma((double)dl, dc, -mq), S.table);
-      if (op != OP_SUMS) {
-        v *= iP;
-        const double qq = q * iQ;
-        for (int k = 0; k < rounds - 1; ++k) v = fmax(v - qq, 0.0) / S.Z[k];
-        v = fmax(v - qq, 0.0);
-      } else {
-        for (int k = 0; k < n_gone; ++k)
-          if (S.token[S.gone[k]] == j) v = 0.0;
-      }
-      return v;
-    };
-    const bool t_vec = (reinterpret_cast<uintptr_t>(tp + lo) & (4 * sizeof(T) - 1)) == 0;
-    const bool d_vec = (reinterpret_cast<uintptr_t>(dp + lo) & (4 * sizeof(T) - 1)) == 0;
+    const double iP = S.iP, iQ = S.iQ;
     auto load4 = [&](const T* row, bool vec, int j, float* x) {
-      if (vec && j + 4 <= hi) {
+      if (vec && j >= 0 && j + 4 <= hi) {
         if constexpr (sizeof(T) == 4) {
           const float4 v = *reinterpret_cast<const float4*>(row + j);
           x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
@@ -362,64 +447,120 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = j + k < hi ? to_f(row[j + k]) : -INFINITY;
+        for (int k = 0; k < 4; ++k) x[k] = j + k >= 0 && j + k < hi ? to_f(row[j + k]) : -INFINITY;
       }
     };
-    double sv = 0.0, sq = 0.0, full = 0.0;
-    for (int s = 0, j = lo + tid * 4; lo + s * kPass < hi; ++s, j += kPass) {
-      float tl[4], dl[4] = {0.f, 0.f, 0.f, 0.f};
-      load4(tp, t_vec, j, tl);
-      if (wants_q) load4(dp, d_vec, j, dl);
-      double v = 0.0;
+    // Rejections one after another start from what the pass before kept, not from the logits.
+    const bool store = sampled && P.keep > 0;
+    const bool from_kept = store && op == OP_REST && S.kept == rounds - 1;
+    const bool q_from_kept = from_kept && P.keep > 1;
+    const double scale = rounds > 1 ? S.iZ[rounds > 1 ? rounds - 2 : 0] : iP;
+    double sv = 0.0, sq = 0.0;
+#pragma unroll 1
+    for (int s = 0, j = lo + tid * kPer; lo + s * kPass < hi; ++s, j += kPass) {
+      double v[kPer], q[kPer];
+      float tl[kPer], dl[kPer];
+      double* const at_v = kept_v + s * kPass;
+      double* const at_q = kept_q + s * kPass;
+      if (!from_kept)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        double q = 0.0;
-        v += value(j + k, tl[k], dl[k], q);
-        sq += q;
+        for (int k = 0; k < kPer; k += 4) load4(tp, true, j + k, tl + k);
+      if (sampled && !q_from_kept)
+#pragma unroll
+        for (int k = 0; k < kPer; k += 4) load4(dp, d_vec, j + k, dl + k);
+      if (from_kept) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[k] = at_v[k * kThreads];
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[k] = exp2_table(fma((double)tl[k], tc, mp), (tl[k] - mtf) * tcf <= -1000.f, S.table);
       }
-      sv += v;
+      if (sampled) {
+        if (q_from_kept) {
 #pragma unroll
-      for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (lane == 0) piece[s * kWarps + warp] = v;
+          for (int k = 0; k < kPer; ++k) q[k] = at_q[k * kThreads];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) q[k] = exp2_table(fma((double)dl[k], dc, mq), (dl[k] - mdf) * dcf <= -1000.f, S.table);
+          if (P.keep > 1)
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) at_q[k * kThreads] = q[k];
+        }
+        if (rounds == 0) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) sq += q[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) q[k] *= iQ;
+          // all rejections so far, or only the last one
+#pragma unroll 1
+          for (int y = from_kept ? rounds - 1 : 0; y < rounds; ++y) {
+            const double f = from_kept ? scale : y == 0 ? iP : S.iZ[y - 1];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              v[k] = v[k] * f - q[k];
+              if (v[k] < 0.0) v[k] = 0.0;
+            }
+          }
+        }
+        if (store)
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) at_v[k * kThreads] = v[k];
+      } else {
+        for (int y = 0; y < n_gone; ++y) {
+          const int at = S.token[S.gone[y]] - j;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            if (at == k) v[k] = 0.0;
+        }
+      }
+      double w = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+#pragma unroll
+      for (int off = 16; off; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+      if (lane == 0) piece[s * kWarps + warp] = w;
+      sv += w;
     }
-    // what was taken out of P belongs to the sum of its exponentials
-    if (op == OP_SUMS && rank == 0 && tid == 0)
-      for (int k = 0; k < n_gone; ++k) full += S.p[S.gone[k]];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, off);
+    if (lane == 0) S.warp_sum[0][warp] = sv, S.warp_sum[1][warp] = sq;
     const int slot = turn++ & 1;
-    for (int y = 0; y < 2; ++y) {
-      double x = y ? sq : sv;
+    __syncthreads();
+    if (warp < 2) {
+      double x = lane < kWarps ? S.warp_sum[warp][lane] : 0.0;
 #pragma unroll
       for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-      if (lane == 0) S.warp_sum[warp] = x;
-      __syncthreads();
-      if (tid < (int)C) {
-        double t = 0.0;
-        for (int k = 0; k < kWarps; ++k) t += S.warp_sum[k];
-        st_peer_f64(mapa(smem_u32(&S.sums[slot][y][rank]), tid), t);
-      }
-      __syncthreads();
+      if (lane < (int)C) st_peer_f64(mapa(smem_u32(&S.sums[slot][warp][rank]), lane), x);
     }
-    if (tid < (int)C) st_peer_f64(mapa(smem_u32(&S.sums[slot][2][rank]), tid), __shfl_sync((1u << C) - 1u, full, 0));
     cluster_sync();
-    if (tid == 0) {
-      double t[3] = {0.0, 0.0, 0.0};
-      for (int y = 0; y < 3; ++y)
-        for (int k = 0; k < (int)C; ++k) t[y] += S.sums[slot][y][k];
-      S.total[0] = t[0];
-      if (op == OP_SUMS) {
-        S.ZP = t[0] + t[2], S.ZQ = t[1];
-        exact = true;
-        summed = true;
-      } else if (op == OP_AGAIN) {
-        summed = true;
-      } else {
-        // (a sum that is NaN counts as something: the draw then finds no distribution)
-        summed = !(t[0] <= 0.0);
-        if (summed) S.Z[S.rounds++] = t[0];  // else nothing would be left: P stays
-        ++c;  // this child is dealt with
+    if (warp == 0) {
+      double t = lane < (int)C ? S.sums[slot][0][lane] : 0.0, z = lane < (int)C ? S.sums[slot][1][lane] : 0.0;
+#pragma unroll
+      for (int off = kMaxCluster / 2; off; off >>= 1) {
+        t += __shfl_xor_sync(0xffffffffu, t, off);
+        z += __shfl_xor_sync(0xffffffffu, z, off);
+      }
+      if (lane == 0) {
+        S.total = t;
+        if (op == OP_SUMS) {
+          // what was taken out of P belongs to the sum of its exponentials
+          for (int k = 0; k < S.n_gone; ++k) t += S.p[S.gone[k]];
+          S.iP = 1.0 / t, S.iQ = 1.0 / z;
+          exact = summed = true;
+          left = 1.0;
+          for (int k = 0; k < S.n_gone; ++k) left -= S.p[S.gone[k]] * S.iP;
+          S.kept = 0;
+        } else if (op == OP_AGAIN) {
+          summed = true;
+          S.kept = S.rounds;
+        } else {
+          // (a sum that is NaN counts as something: the draw then finds no distribution)
+          summed = !(t <= 0.0);
+          if (summed) S.iZ[S.rounds++] = 1.0 / t;  // else nothing would be left: P stays
+          S.kept = summed ? S.rounds : -1;
+          ++c;  // this child is dealt with
+        }
       }
     }
-    __syncthreads();
   }
 
   // ---- the draw: `piece` and S.sums hold the final P, unscaled, in order ----
@@ -430,24 +571,27 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   }
   if (greedy || nn == 0) {
     if (tid == 0 && rank == 0) P.next_token[b] = nn > 0 && S.idx[S.cur] < V ? S.idx[S.cur] : -1;
-  } else {
+  } else if (warp == 0) {
     const int slot = (turn - 1) & 1;
-    const double total = S.total[0], want = P.r[b] > 0.f ? (double)P.r[b] * total : 0.0;
+    const double total = S.total, want = P.r[b] > 0.f ? (double)P.r[b] * total : 0.0;
     double before = 0.0;  // of the blocks before this one
-    for (int k = 0; k < (int)rank; ++k) before += S.sums[slot][0][k];
-    const double mine = S.sums[slot][0][rank];
-    int last = -1;  // the last block with any P: takes what rounding leaves over
-    for (int k = 0; k < (int)C; ++k)
+    int last = -1;        // the last block with any P: takes what rounding leaves over
+    for (int k = 0; k < (int)C; ++k) {
+      if (k < (int)rank) before += S.sums[slot][0][k];
       if (S.sums[slot][0][k] > 0.0) last = k;
-    const bool fits = total > 0.0 && total < INFINITY;
-    if (!fits) {
+    }
+    const double mine = S.sums[slot][0][rank];
+    if (!(total > 0.0 && total < INFINITY)) {
       if (tid == 0 && rank == 0) P.next_token[b] = -1;  // no distribution
-    } else if (warp == 0 && before <= want && (before + mine > want || (int)rank == last) && mine > 0.0) {
-      // pieces of 128 elements, then the elements of one piece
+    } else if (before <= want && (before + mine > want || (int)rank == last) && mine > 0.0) {
+      // pieces of 32 kPer elements, then the elements of one piece
+      const T* tp = target + S.cur * P.t_node;
+      const T* dp = draft + (sampled ? S.cur * P.d_node : 0);
+      const int lead = (int)((reinterpret_cast<uintptr_t>(tp) / sizeof(T)) & 3);
+      const int lo = (int)rank * slice - lead, hi = min(V, lo + slice);
       const int n_piece = (hi - lo + kPass - 1) / kPass * kWarps;
-      int at = -1;
+      int at = -1, keep = -1;
       double base = before, sure = before;
-      int keep = -1;
       for (int k0 = 0; k0 < n_piece && at < 0; k0 += 32) {
         const double x = k0 + lane < n_piece ? piece[k0 + lane] : 0.0;
         double cum = x;
@@ -474,24 +618,30 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       if (at < 0) at = keep, base = sure;
       // the rows once more, as the last pass saw them
       const int rounds = S.rounds;
-      const T* tp = target + S.cur * P.t_node;
-      const T* dp = draft + (sampled ? S.cur * P.d_node : 0);
-      const double mp = (double)S.m[0][S.cur] * tc, mq = sampled ? (double)S.m[1][S.cur] * dc : 0.0;
-      double v[4], sum = 0.0;
-      const int j = lo + at / kWarps * kPass + at % kWarps * 128 + lane * 4;
+      const float mtf = S.m[0][S.cur], mdf = S.m[1][S.cur];
+      const double mp = -((double)mtf * tc), mq = -((double)mdf * dc);
+      double v[kPer], sum = 0.0;
+      const int j = lo + at / kWarps * kPass + (at % kWarps * 32 + lane) * kPer;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kPer; ++k) {
         v[k] = 0.0;
-        if (j + k < hi) {
-          v[k] = exp2_table(fma((double)to_f(tp[j + k]), tc, -mp), S.table);
-          if (rounds > 0) {
-            const double qq = exp2_table(fma((double)to_f(dp[j + k]), dc, -mq), S.table) * (1.0 / S.ZQ);
-            v[k] *= 1.0 / S.ZP;
-            for (int y = 0; y < rounds - 1; ++y) v[k] = fmax(v[k] - qq, 0.0) / S.Z[y];
-            v[k] = fmax(v[k] - qq, 0.0);
+        if (j + k >= 0 && j + k < hi) {
+          if (sampled && P.keep > 0 && S.kept == rounds) {
+            v[k] = dyn[(at / kWarps * kPer + k) * kThreads + at % kWarps * 32 + lane];
           } else {
-            for (int y = 0; y < S.n_gone; ++y)
-              if (S.token[S.gone[y]] == j + k) v[k] = 0.0;
+            const float tl = to_f(tp[j + k]);
+            v[k] = exp2_table(fma((double)tl, tc, mp), (tl - mtf) * tcf <= -1000.f, S.table);
+            if (rounds > 0) {
+              const float dl = to_f(dp[j + k]);
+              const double q = exp2_table(fma((double)dl, dc, mq), (dl - mdf) * dcf <= -1000.f, S.table) * S.iQ;
+              for (int y = 0; y < rounds; ++y) {
+                v[k] = v[k] * (y == 0 ? S.iP : S.iZ[y - 1]) - q;
+                if (v[k] < 0.0) v[k] = 0.0;
+              }
+            } else {
+              for (int y = 0; y < S.n_gone; ++y)
+                if (S.token[S.gone[y]] == j + k) v[k] = 0.0;
+            }
           }
         }
         sum += v[k];
@@ -503,21 +653,18 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         if (lane >= off) cum += o;
       }
       double run = base + (cum - sum);
-      int mineat = 0x7fffffff, lastat = -1;
+      int hit = 0x7fffffff, any = -1;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kPer; ++k) {
         run += v[k];
         if (v[k] > 0.0) {
-          lastat = j + k;
-          if (run > want && mineat == 0x7fffffff) mineat = j + k;
+          any = j + k;
+          if (run > want && hit == 0x7fffffff) hit = j + k;
         }
       }
-#pragma unroll
-      for (int off = 16; off; off >>= 1) {
-        mineat = min(mineat, __shfl_xor_sync(0xffffffffu, mineat, off));
-        lastat = max(lastat, __shfl_xor_sync(0xffffffffu, lastat, off));
-      }
-      if (lane == 0) P.next_token[b] = mineat != 0x7fffffff ? mineat : lastat;
+      hit = __reduce_min_sync(0xffffffffu, hit);
+      any = __reduce_max_sync(0xffffffffu, any);
+      if (lane == 0) P.next_token[b] = hit != 0x7fffffff ? hit : any;
     }
   }
   cluster_sync();  // no block leaves while a peer may still store into it
@@ -531,7 +678,7 @@ size_t tree_verify_workspace_bytes(int B, int n, int V) {
 }
 
 template <typename T>
-static cudaError_t verify_launch(const verify::Params& P, cudaStream_t stream) {
+static cudaError_t verify_launch(verify::Params P, cudaStream_t stream) {
   using namespace verify;
   static std::atomic<int> largest[64];
   int dev = 0;
@@ -552,8 +699,9 @@ static cudaError_t verify_launch(const verify::Params& P, cudaStream_t stream) {
   int most = dev < 64 ? largest[dev].load() : 0;
   if (!most) {
     e = cudaFuncSetAttribute(walk<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(walk<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(walk<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDyn);
     if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = kMaxDyn;
     cfg.numAttrs = 1;
     attr[0].val.clusterDim.x = kMaxCluster;
     cfg.gridDim = dim3(kMaxCluster);
@@ -568,9 +716,12 @@ static cudaError_t verify_launch(const verify::Params& P, cudaStream_t stream) {
   // A sequence's walk waits for its own passes: as many blocks as the batch leaves room for.
   int C = P.B * 16 <= 128 ? most : 8;
   while (C > 1 && (int64_t)(C - 1) * kPass >= P.V) C /= 2;
-  const int slice = ((P.V + C - 1) / C + 3) & ~3;
-  cfg.dynamicSmemBytes = (size_t)(slice + kPass - 1) / kPass * kWarps * sizeof(double);
-  if (cfg.dynamicSmemBytes > 128 * 1024) return cudaErrorInvalidValue;
+  // shared memory as the kernel lays it out
+  const int slice = ((P.V + 3 + C - 1) / C + 3) & ~3, steps = (slice + kPass - 1) / kPass;
+  const size_t row = (size_t)steps * kPass * sizeof(double), pieces = (size_t)steps * kWarps * sizeof(double);
+  P.keep = !P.draft ? 0 : 2 * row + pieces <= kMaxDyn ? 2 : row + pieces <= kMaxDyn ? 1 : 0;
+  cfg.dynamicSmemBytes = P.keep * row + pieces;
+  if (cfg.dynamicSmemBytes > kMaxDyn) return cudaErrorInvalidValue;
   attr[0].val.clusterDim.x = C;
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(C * P.B);

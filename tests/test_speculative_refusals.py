@@ -47,7 +47,7 @@ def verify(kw_shape=None, **kw):
     return mk._lib.mk_tree_verify(ctypes.byref(mk.mk_verify_shape(**s)), *a.values(), None)
 
 
-@pytest.mark.parametrize("kw", [dict(dtype=3), dict(B=0), dict(n=0), dict(n=257), dict(vocab=0), dict(vocab=(1 << 23) + 1),
+@pytest.mark.parametrize("kw", [dict(dtype=3), dict(B=0), dict(n=0), dict(n=257), dict(vocab=0), dict(vocab=(1 << 20) + 1),
                                 dict(B=70000, n=1), dict(t_seq=-1), dict(t_node=-8), dict(d_node=-1)])
 def test_tree_verify_shapes(kw):
     assert verify(kw) == mk.MK_ERR_INVALID_ARG

@@ -395,11 +395,13 @@ _TREE_SHAPE = struct.Struct("7i4x12q")
 _VERIFY_SHAPE = struct.Struct("4i4q")
 _CACHE_SHAPE = struct.Struct("6i")
 _types = None  # (torch, {dtype: code}): torch is only imported by the calls that take tensors
+_devices = 0
 
 
 def _torch_types():
-    global _types
+    global _types, _devices
     import torch
+    _devices = torch.cuda.device_count()
     # int16 holds bf16 bits (Megakernel.kv_view)
     _types = (torch, {torch.bfloat16: MK_BF16, torch.int16: MK_BF16, torch.float16: MK_FP16, torch.float32: MK_FP32})
     return _types
@@ -426,7 +428,7 @@ def _call(torch, f, tensors, *args):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             _refuse(f"tensors on {tensors[0].device} and {t.device}")
-    if torch.cuda.current_device() == dev:
+    if _devices == 1 or torch.cuda.current_device() == dev:
         rc = f(*args)
     else:
         with torch.cuda.device(dev):

@@ -85,31 +85,35 @@ __global__ void __launch_bounds__(kThreads) commit(const Params P) {
 // a row that several sequences take is read once.
 constexpr int kB = MK_MAX_BATCH;
 
-template <int N, int U>
-__device__ __forceinline__ void move_places(const Params& P, uint4* p, int64_t at, int64_t step, int64_t end,
-                                            int distinct, const int* from, const int* upto, const uint32_t* to) {
-  // N: sequences read at most; U: places of a thread in flight
-  for (; at < end; at += step * U) {
-    uint4 v[U][N];
+// V: what a thread takes of a place (16 bytes, or 8 where many sequences are read: the values of
+// all of them are in registers at once, and fewer registers keep four blocks on an SM).
+// N: sequences read at most; U: places of a thread in flight.
+template <typename V, int N, int U>
+__device__ __forceinline__ void move_places(const Params& P, V* p, int64_t at, int64_t step, int64_t end, int distinct,
+                                            const int* from, const int* upto, const uint32_t* to) {
+  constexpr int kPer = sizeof(uint4) / sizeof(V);
+  const int64_t seq = P.seq * kPer;
+  for (; at < end * kPer; at += step * U) {
+    V v[U][N];
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
       for (int y = 0; y < N; ++y) {
         const int64_t a = at + k * step;
-        if (y < distinct && a < upto[y] && a < end) v[k][y] = p[from[y] * P.seq + a];
+        if (y < distinct && a < (int64_t)upto[y] * kPer) v[k][y] = p[from[y] * seq + a];
       }
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
       for (int y = 0; y < N; ++y) {
         const int64_t a = at + k * step;
-        if (y < distinct && a < upto[y] && a < end)
-          for (uint32_t set = to[y]; set; set &= set - 1) p[(__ffs(set) - 1) * P.seq + a] = v[k][y];
+        if (y < distinct && a < (int64_t)upto[y] * kPer)
+          for (uint32_t set = to[y]; set; set &= set - 1) p[(__ffs(set) - 1) * seq + a] = v[k][y];
       }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) reorder(const Params P) {
+__global__ void __launch_bounds__(kThreads, 3) reorder(const Params P) {
   __shared__ int from[kB], upto[kB];   // sequences to read, and how many pieces of each
   __shared__ uint32_t to[kB];          // the sequences that take them
   __shared__ int s_distinct, s_most;
@@ -141,11 +145,13 @@ __global__ void __launch_bounds__(kThreads) reorder(const Params P) {
     uint4* p = P.base + (lk >> 1) * P.layer + (lk & 1) * P.kv + h * P.head;
     const int64_t at = (int64_t)blockIdx.x * kThreads + tid;
     if (distinct == 1)
-      move_places<1, 4>(P, p, at, step, most, distinct, from, upto, to);
+      move_places<uint4, 1, 4>(P, p, at, step, most, distinct, from, upto, to);
     else if (distinct <= 4)
-      move_places<4, 2>(P, p, at, step, most, distinct, from, upto, to);
+      move_places<uint4, 4, 1>(P, p, at, step, most, distinct, from, upto, to);
+    else if (distinct <= 8)
+      move_places<uint4, 8, 1>(P, p, at, step, most, distinct, from, upto, to);
     else
-      move_places<kB, 1>(P, p, at, step, most, distinct, from, upto, to);
+      move_places<uint2, kB, 1>(P, reinterpret_cast<uint2*>(p), at, step, most, distinct, from, upto, to);
   }
 }
 

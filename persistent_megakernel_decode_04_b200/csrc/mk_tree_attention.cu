@@ -6,18 +6,18 @@
 //
 // Mapping.  The G query heads of a KV head and the nodes share their keys, so they are the rows
 // of one matrix product: a row tile is 128 rows (floor(128 / G) nodes x G heads) and both
-// products run on the tensor cores (M = 128, fp32 accumulators in TMEM): S = Q K^T over 128-key
-// tiles, O += P V with P as the TMEM operand.  K tiles are K-major, V tiles MN-major, both as
-// TMA writes them with the 128-byte swizzle.  128 rows cost the same as 1: a 128-key tile takes
-// the tensor cores 2 x 0.13 us, while its 64 KB take an SM's share of HBM 1.4 us.
+// products run on the tensor cores (M = 128, fp32 accumulators in TMEM): S = Q K^T over 64-key
+// tiles, O += P V with P as the TMEM operand.  K tiles are K-major, V tiles MN-major, both as TMA
+// writes them with the 128-byte swizzle.  128 rows cost the same as 1: a tile (128 values per key)
+// takes the tensor cores about 0.2 us, while its 32 KB take an SM's share of HBM 0.7 us.
 //
-// A block holds one row tile (two blocks per SM, so that one block's start, end and softmax run
-// beside the other's loads and products) or, for more than 128 rows, two row tiles that share
-// every key tile (one block per SM: half the reads from L2).  Each row tile has four softmax
-// warps; one warp issues the loads, one the products, and two helpers prepare the tree: the
-// ancestor bits of every node, and V tiles that end the sequence.
+// A block holds one row tile; two blocks share an SM, so that one's start, end and softmax run
+// beside the other's loads and products.  (Two row tiles per block that share every key tile, one
+// block per SM, read L2 half as often and were slower: 156 us against 140 for 8 x 256 nodes.)  Four
+// warps do the softmax, one issues the loads, one the products, and two helpers prepare the tree:
+// the ancestor bits of every node, and V tiles that end the sequence.
 //
-// The keys of a (sequence, KV head, row tiles) unit are split over a thread-block cluster, whose
+// The keys of a (sequence, KV head, row tile) unit are split over a thread-block cluster, whose
 // blocks merge their partial results through distributed shared memory: no workspace, no
 // atomics, a fixed order of summation.
 //
@@ -38,28 +38,32 @@
 namespace mk {
 namespace tree {
 
-constexpr int kKeys = 128;        // keys per tile
+constexpr int kKeys = 64;         // keys per tile
 constexpr int kRows = 128;        // rows per row tile
 constexpr int kMaxNodes = MK_MAX_TREE_NODES;
 constexpr int kAncStride = kMaxNodes / 32 + 1;  // odd: rows fall on different banks
 constexpr int kMaxCluster = 16;
-constexpr int kCh = 32;            // keys of a row of S in registers at a time
 
-// NT: row tiles of a block (1 or 2).
-template <int D, int NT>
+constexpr int kSoft = 4;          // softmax warps; then loads, products, two helpers
+constexpr int kTmaWarp = 4, kMmaWarp = 5, kHelper = 6;
+constexpr int kThreads = 256;
+
+template <int D>
 struct Geo {
-  static constexpr int kSoft = 8 * NT;             // softmax warps; then loads, products, two helpers
-  static constexpr int kThreads = (kSoft + 4) * 32;
-  static constexpr int kTile = kKeys * D * 2;      // bytes of a K, V or Q tile
-  static constexpr int kStages = (NT == 1 ? 2 : 4) * (128 / D) + (NT == 1 && D == 64 ? 1 : 0);
+  static constexpr int kTile = kKeys * D * 2;      // bytes of a K or V tile
+  static constexpr int kQTile = kRows * D * 2;
+  static constexpr int kStages = 4 * (128 / D);
+  static constexpr int kData = kQTile + kStages * kTile;
   static constexpr int kOStride = D + 4;           // floats: 16-byte rows, no bank conflicts
-  static constexpr int kData = (NT + kStages) * kTile;
-  // Tensor memory: S_w at w * 128 (P over it: keys 0..63 at 0, 64..127 at 64), O_w at NT * 128 + w * D
-  static constexpr uint32_t kCols = NT * 256;
+  // Behind the partial O's (over Q and the ring): a warp's 32 rows x 32 columns on their way out
+  static constexpr int kStageStride = 36;
+  static constexpr int kStageAt = (kRows + kMaxCluster) * kOStride * 4;
+  static_assert(kStageAt + kSoft * 32 * kStageStride * 4 <= kData, "partial O's and stages fit over Q and the ring");
+  // Tensor memory: S of even and odd tiles at 0 and 64 (P over the first half of each), O at 128.
   // Shared memory bounds the blocks per SM to 512 / kCols: one more would wait for tensor memory
   // while its cluster's other blocks hold theirs.
-  static_assert(NT == 1 ? kData > 76 * 1024 : kData > 116 * 1024, "blocks per SM");
-  static_assert(NT * kRows * kOStride * 4 <= kData, "partial O fits over Q and the ring");
+  static constexpr uint32_t kCols = 256;
+  static_assert(kData > 76 * 1024, "two blocks per SM");
 };
 
 struct Params {
@@ -70,7 +74,7 @@ struct Params {
   int64_t q_seq, q_node, q_head, o_seq, o_node, o_head, v_seq, v_head, v_row;
   int n, hq, hkv, G, max_seq;
   int nt;        // nodes per row tile
-  int units;     // blocks' worth of row tiles per (sequence, KV head)
+  int units;     // row tiles per (sequence, KV head)
   uint32_t inv_g;  // r / G = r * inv_g >> 16 for r < 256
   float c;       // |scale| * log2(e)
   uint32_t negate; // scale < 0: the product takes -Q (a bit of the instruction descriptor)
@@ -79,16 +83,15 @@ struct Params {
 };
 
 struct Ctl {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_full, q_full, mma_done, anc_full;
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done, o_full, q_full, mma_done, anc_full;
   uint32_t tmem, abort;
   uint32_t bad_v;  // infinite or NaN values among the drafts that this block saw
   // Counters that only grow, for roles that may be more than one step apart (an mbarrier's parity
   // cannot tell two steps from none): V tiles to clean that were issued; helpers' shares done.
   uint32_t v_issued, v_clean;
   uint32_t bad_any;  // some block of the cluster has bad_v set
-  float pair[2][2][2 * kRows];  // what the two threads of a row tell each other, by turns
   // (maximum, sum) of every row that this block finishes from every block of the cluster
-  float2 stat[2 * kRows + kMaxCluster];
+  float2 stat[kRows + kMaxCluster];
   uint32_t anc[kMaxNodes * kAncStride];
 };
 
@@ -122,6 +125,7 @@ __device__ __forceinline__ bool wait_count(const uint32_t* at, uint32_t value, c
   if ((int32_t)(ld_acquire_cta_shared(at) - value) >= 0) return true;
   const uint64_t t0 = globaltimer_ns();
   while ((int32_t)(ld_acquire_cta_shared(at) - value) < 0) {
+    __nanosleep(40);
     if (*reinterpret_cast<volatile uint32_t*>(&S.abort)) return false;
     if (globaltimer_ns() - t0 > P.timeout_ns) {
       *reinterpret_cast<volatile uint32_t*>(&S.abort) = 1;
@@ -154,6 +158,14 @@ __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo, uint32
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The products are issued by one thread, but the whole warp walks the loop around them: the waits
+// and the descriptors are the same for every lane then and stay in uniform registers.  (In a loop
+// of one lane each instruction cost about 80 cycles to issue, more than it runs.)
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // D[tmem] (+)= A[tmem] . B[smem desc], one thread.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accum) {
@@ -237,7 +249,7 @@ __device__ __forceinline__ float value16(uint16_t h) {
   return __uint_as_float((uint32_t)h << 16);
 }
 
-// Address of a peer CTA's shared memory, and loads from there.
+// Address of a peer block's shared memory, and stores there.
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -249,13 +261,9 @@ __device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t x) {
 __device__ __forceinline__ void st_peer_f2(uint32_t addr, float x, float y) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
-__device__ __forceinline__ float4 ld_peer_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+__device__ __forceinline__ void st_peer_v4(uint32_t addr, const uint4& x) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                : "memory");
-  return v;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -280,6 +288,10 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t* anc, int rel0) {
   const uint32_t hi = w + 1 < kMaxNodes / 32 ? anc[w + 1] : 0u;
   return __funnelshift_r(anc[w], hi, rel0 & 31);
 }
+
+// Loads run K two tiles ahead of V: K 0, K 1, V 0, K 2, V 1, ..: where K and V of tile j come, of T tiles.
+__device__ __forceinline__ int k_index(int j) { return j < 2 ? j : 2 * j - 1; }
+__device__ __forceinline__ int v_index(int j, int T) { return j + min(T, j + 2); }
 
 // Ancestor bits (self included) of nodes 0..nn-1, one warp, 32 nodes at a time.  Within the block
 // of 32 by doubling: a node takes over the bits of the node it points at, and then points where
@@ -334,18 +346,18 @@ __device__ __noinline__ void add_nonfinite(const Params& P, const Ctl& S, int b,
   }
 }
 
-// Output rows that this block finishes: row r's partial results, weighted, from the C blocks.
-// The loops are kept rolled: this runs once, and its instructions come from memory.
-template <int D, bool FP16, int NT>
-__device__ __forceinline__ void merge(const Params& P, const Ctl& S, const uint8_t* data, int b, int h, int first,
+// Output rows that this block finishes: row r's partial results, weighted, from the C blocks (they
+// lie in this block's shared memory: part p of its x-th row at row p * per + x).  The loops are kept
+// rolled: this runs once, and its instructions come from memory.
+template <int D, bool FP16>
+__device__ __forceinline__ void merge(const Params& P, const Ctl& S, const float* parts, int b, int h, int first,
                                       int rows, int per, int rank, int C, int len, int warp, int lane) {
-  using Ge = Geo<D, NT>;
+  using Ge = Geo<D>;
   constexpr int kLanes = D / 4, kPer = 32 / kLanes;  // lanes per row, rows per warp side by side
   const int sub = lane / kLanes, in = lane % kLanes, col = in * 4;
-  const int r0 = rank * per, r1 = min(rows, r0 + per), tile_rows = P.nt * P.G;
-  if (r0 >= r1) return;
+  const int r0 = rank * per, r1 = min(rows, r0 + per);
 #pragma unroll 1
-  for (int base = r0 + warp * kPer; base < r1; base += Ge::kThreads / 32 * kPer) {
+  for (int base = r0 + warp * kPer; base < r1; base += kThreads / 32 * kPer) {
     const int r = min(base + sub, r1 - 1);
     // lane p of the row's group holds part p's weight (C <= 16 <= kLanes)
     const float2 st = S.stat[(r - r0) * C + (in & (C - 1))];
@@ -355,28 +367,19 @@ __device__ __forceinline__ void merge(const Params& P, const Ctl& S, const uint8
     float f = st.x == -INFINITY && st.y == 0.f ? 0.f : mx == -INFINITY ? 1.f : ex2((st.x - mx) * P.c);
     float sum = st.y * f;
     for (int off = C / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const int t = NT == 2 && r >= tile_rows, lr = r - t * tile_rows;
-    const int local = (int)(lr * P.inv_g >> 16), g = lr - local * P.G, node = first + t * P.nt + local;
+    const int local = (int)(r * P.inv_g >> 16), g = r - local * P.G, node = first + local;
     f = sum == 0.f || !alive(S, node) ? 0.f : __fdividef(f, sum);
-    const uint32_t src = smem_u32(data) + (uint32_t)(((t * kRows + lr) * Ge::kOStride + col) * 4);
+    const float* src = parts + (r - r0) * Ge::kOStride + col;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (int p0 = 0; p0 < C; p0 += 8) {
-      float fp[8];
-      float4 v[8];
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {  // eight loads in flight
-        fp[p] = __shfl_sync(0xffffffffu, f, p0 + p, kLanes);
-        v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p0 + p >= C) fp[p] = 0.f;
-        if (fp[p] != 0.f) v[p] = ld_peer_f4(mapa(src, p0 + p));
-      }
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        acc[0] = fmaf(fp[p], v[p].x, acc[0]);
-        acc[1] = fmaf(fp[p], v[p].y, acc[1]);
-        acc[2] = fmaf(fp[p], v[p].z, acc[2]);
-        acc[3] = fmaf(fp[p], v[p].w, acc[3]);
+#pragma unroll 4
+    for (int p = 0; p < C; ++p) {
+      const float fp = __shfl_sync(0xffffffffu, f, p, kLanes);
+      const float4 v = *reinterpret_cast<const float4*>(src + p * per * Ge::kOStride);
+      if (fp != 0.f) {
+        acc[0] = fmaf(fp, v.x, acc[0]);
+        acc[1] = fmaf(fp, v.y, acc[1]);
+        acc[2] = fmaf(fp, v.z, acc[2]);
+        acc[3] = fmaf(fp, v.w, acc[3]);
       }
     }
     if (base + sub >= r1) continue;
@@ -386,43 +389,43 @@ __device__ __forceinline__ void merge(const Params& P, const Ctl& S, const uint8
   }
 }
 
-template <int D, bool FP16, int NT>
-__global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 2)
     tree_attention(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ Params P) {
-  using Ge = Geo<D, NT>;
+  using Ge = Geo<D>;
   extern __shared__ uint8_t raw[];
   __shared__ Ctl S;
-  constexpr int kTmaWarp = Ge::kSoft, kMmaWarp = Ge::kSoft + 1, kHelper = Ge::kSoft + 2;
   uint8_t* data = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t* ring = data + NT * Ge::kTile;
+  uint8_t* ring = data + Ge::kQTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
 
   const int unit = blockIdx.x / C, head = unit / P.units;
   const int b = head / P.hkv, h = head - b * P.hkv;
-  const int first = (unit - head * P.units) * NT * P.nt;  // first node of the block's row tiles
+  const int first = (unit - head * P.units) * P.nt;  // first node of the block's row tile
   int len = P.lens[b], nn = P.n_nodes ? P.n_nodes[b] : P.n;
-  // softmax warps: row tile, row, and which half of a tile's keys (and of O's columns) of that row
-  const int w = warp >> 3, row = tid & 127, half = (warp >> 2) & 1;
+  const int row = tid & 127;  // of a softmax thread
   const int local = (int)(row * P.inv_g >> 16);
 
   // ---- start: whatever does not need the lengths first ----
   int parent = -1;
   if (warp == kTmaWarp) {
     if (lane == 0) {
+      prefetch_tensormap(&map_k);
+      prefetch_tensormap(&map_v);
 #pragma unroll 1
       for (int i = 0; i < Ge::kStages; ++i) {
         mbar_init(&S.full[i], 1);
         mbar_init(&S.empty[i], 1);
       }
-#pragma unroll 1
-      for (int i = 0; i < NT; ++i) {
+      for (int i = 0; i < 2; ++i) {
         mbar_init(&S.s_full[i], 1);
-        mbar_init(&S.p_full[i], 8);
+        mbar_init(&S.p_full[i], kSoft);
       }
+      mbar_init(&S.o_done, 1);
       mbar_init(&S.o_full, 1);
-      mbar_init(&S.q_full, Ge::kSoft);
+      mbar_init(&S.q_full, kSoft);
       mbar_init(&S.mma_done, 1);
       mbar_init(&S.anc_full, 1);
       S.abort = S.bad_v = S.bad_any = S.v_issued = S.v_clean = 0;
@@ -433,15 +436,15 @@ __global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
     tc_relinquish();
   } else if (warp == kHelper) {
     if (lane < P.n) parent = P.parents[(int64_t)b * P.n + lane];
-  } else if (warp < Ge::kSoft) {
+  } else if (warp < kSoft) {
     // Q rows into the swizzled tile: 16-byte piece c of row r goes to piece c ^ (r % 8).  Rows of
     // the tile without a node keep what is there: they only reach their own, unused, results.
-    const int x0 = tid & 255, c = x0 % (D / 8), used = min(P.nt, P.n - first - w * P.nt) * P.G;
-    const uint16_t* src = P.q + (int64_t)b * P.q_seq + (int64_t)(first + w * P.nt) * P.q_node +
+    const int c = row % (D / 8), used = min(P.nt, P.n - first) * P.G;
+    const uint16_t* src = P.q + (int64_t)b * P.q_seq + (int64_t)first * P.q_node +
                           (int64_t)h * P.G * P.q_head + c * 8;
-    const uint32_t dst = smem_u32(data) + w * Ge::kTile + (c / 8) * kRows * 128;
+    const uint32_t dst = smem_u32(data) + (c / 8) * kRows * 128;
 #pragma unroll 1
-    for (int r = x0 / (D / 8); r < used; r += 2 * kRows / (D / 8)) {
+    for (int r = row / (D / 8); r < used; r += kRows / (D / 8)) {
       const int lr = (int)(r * P.inv_g >> 16);
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + r * 128 + ((c & 7) ^ (r & 7)) * 16),
                    "l"(src + (int64_t)lr * P.q_node + (int64_t)(r - lr * P.G) * P.q_head)
@@ -452,82 +455,99 @@ __global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (C > 1) cluster_arrive();  // every block of the cluster has started: waited for before the first access
   const uint32_t tmem = S.tmem;
 
   len = min(max(len, 0), P.max_seq), nn = min(min(max(nn, 0), P.n), P.max_seq - len);
   const bool on = first < nn;                      // else there is no node here (the whole cluster alike)
-  const bool two = NT == 2 && first + P.nt < nn;   // the second row tile has nodes
   const int T_all = on ? (len + nn + kKeys - 1) / kKeys : 0;
   const int t0 = rank * T_all / C, T = (rank + 1) * T_all / C - t0;
   const int edge = max(0, len / kKeys - t0);  // first tile of this block that has rows behind len
-  const int rows = min(nn - first, NT * P.nt) * P.G, per = (rows + C - 1) / C;  // rows; of these to finish
+  const int rows = min(nn - first, P.nt) * P.G, per = (rows + C - 1) / C;  // rows; of these to finish
 
   if (warp == kTmaWarp) {
     // ---- loads: K and V of a tile in turn ----
     if (lane == 0 && (int)blockIdx.x != P.drop_block) {
       int x = 0;
-#pragma unroll 1
-      for (; x < 2 * T; ++x) {
+      auto load = [&](const CUtensorMap* map, int tile) {
         const int stage = x % Ge::kStages, use = x / Ge::kStages;
-        if (use > 0 && !wait(&S.empty[stage], (use - 1) & 1, P, S)) break;
+        if (use > 0 && !wait(&S.empty[stage], (use - 1) & 1, P, S)) return false;
         mbar_arrive_expect_tx(&S.full[stage], Ge::kTile);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          tma_4d(ring + stage * Ge::kTile + c * kKeys * 128, x & 1 ? &map_v : &map_k, c * 64, (t0 + (x >> 1)) * kKeys,
-                 h, b, &S.full[stage]);
-        if ((x & 1) && (x >> 1) >= edge) count_up(&S.v_issued);
+          tma_4d(ring + stage * Ge::kTile + c * kKeys * 128, map, c * 64, (t0 + tile) * kKeys, h, b, &S.full[stage]);
+        ++x;
+        return true;
+      };
+#pragma unroll 1
+      for (int j = -2; j < T; ++j) {
+        if (j + 2 < T && j < 0 && !load(&map_k, j + 2)) break;
+        if (j >= 0) {
+          if (!load(&map_v, j)) break;
+          if (j >= edge) count_up(&S.v_issued);
+          if (j + 2 < T && !load(&map_k, j + 2)) break;
+        }
       }
       if (x < 2 * T)  // given up: leave no copy in flight
         for (int y = max(0, x - Ge::kStages); y < x; ++y)
           wait_slow(&S.full[y % Ge::kStages], (y / Ge::kStages) & 1, P.timeout_ns, S, true);
     }
   } else if (warp == kMmaWarp) {
-    // ---- products: one row tile's beside the other's (or the other block's) softmax ----
-    if (lane == 0 && T > 0) {
+    // ---- products ----
+    if (T > 0) {
       constexpr uint32_t type = FP16 ? 0u : 1u;
       constexpr uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(kRows >> 4) << 24);
       const uint32_t idesc_s = idesc | P.negate | ((uint32_t)(kKeys >> 3) << 17);
       constexpr uint32_t idesc_o = idesc | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V is MN-major
-      const uint32_t q_base = smem_u32(data), ring_base = smem_u32(ring);
-      const int last = two ? 1 : 0;
-      bool ok = wait(&S.q_full, 0, P, S);
+      const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
+      const uint64_t q_desc = desc128(smem_u32(data), 16, 1024), k_desc = desc128(smem_u32(ring), 16, 1024),
+                     v_desc = desc128(smem_u32(ring), kKeys * 128, 1024);
+      bool ok = wait_warp(&S.q_full, 0, P, S);
       tc_fence_after();
-      // step y = -1 .. T - 1, for each row tile t: O_t += P_t V of tile y, then S_t = Q_t K^T of tile y + 1
+      // step j = -2 .. T - 1: O += P V of tile j, then S = Q K^T of tile j + 2, over the S and P of
+      // tile j: a tile's scores are there before its softmax can begin
 #pragma unroll 1
-      for (int y = -last - 1; ok && y < (last + 1) * T; ++y) {
-        const int t = (y + last + 1) & last, j = last ? y >> 1 : y;
+      for (int j = -2; ok && j < T; ++j) {
+        const int buf = j & 1;
         if (j >= 0) {
-          const int x = 2 * j + 1, stage = x % Ge::kStages;
-          ok = wait(&S.full[stage], (x / Ge::kStages) & 1, P, S) &&
-               (j < edge || wait_count(&S.v_clean, 2 * (j - edge + 1), P, S)) && wait(&S.p_full[t], j & 1, P, S);
+          const int x = v_index(j, T), stage = x % Ge::kStages;
+          ok = wait_warp(&S.full[stage], (x / Ge::kStages) & 1, P, S) &&
+               (j < edge || wait_count_warp(&S.v_clean, 2 * (j - edge + 1), P, S)) &&
+               wait_warp(&S.p_full[buf], (j >> 1) & 1, P, S);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t bb = ring_base + stage * Ge::kTile;
+          const uint64_t vd = v_desc + (uint32_t)(stage * (Ge::kTile >> 4));
+          if (elect()) {
 #pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            mma_ts(tmem + NT * kKeys + t * D, tmem + t * kKeys + (s & 4) * 16 + (s & 3) * 8, desc128(bb + s * 2048, kKeys * 128, 1024),
-                   idesc_o, j != 0 || s != 0);
-          if (t == last) tc_commit(&S.empty[stage]);
-        }
-        if (j + 1 < T) {
-          const int x = 2 * j + 2, stage = x % Ge::kStages;
-          ok = wait(&S.full[stage], (x / Ge::kStages) & 1, P, S);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = q_base + t * Ge::kTile, bb = ring_base + stage * Ge::kTile;
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = (s / 4) * kKeys * 128 + (s % 4) * 32;
-            tc_mma_f16(tmem + t * kKeys, desc128(a + off, 16, 1024), desc128(bb + off, 16, 1024), idesc_s, s != 0);
+            for (int s = 0; s < kKeys / 16; ++s)
+              mma_ts(tm + 128, tm + buf * 64 + s * 8, vd + s * (2048 >> 4), idesc_o, j != 0 || s != 0);
+            tc_commit(&S.o_done);
+            tc_commit(&S.empty[stage]);
           }
-          tc_commit(&S.s_full[t]);
-          if (t == last) tc_commit(&S.empty[stage]);
+          __syncwarp();
+        }
+        if (j + 2 < T) {
+          const int x = k_index(j + 2), stage = x % Ge::kStages;
+          ok = wait_warp(&S.full[stage], (x / Ge::kStages) & 1, P, S);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = k_desc + (uint32_t)(stage * (Ge::kTile >> 4));
+          if (elect()) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              tc_mma_f16(tm + buf * 64, q_desc + (((s / 4) * kRows * 128 + (s % 4) * 32) >> 4),
+                         kd + (((s / 4) * kKeys * 128 + (s % 4) * 32) >> 4), idesc_s, s != 0);
+            tc_commit(&S.s_full[buf]);
+            tc_commit(&S.empty[stage]);
+          }
+          __syncwarp();
         }
       }
-      if (ok) tc_commit(&S.o_full);
-      tc_commit(&S.mma_done);  // nothing in flight when TMEM is freed
-      wait_slow(&S.mma_done, 0, P.timeout_ns, S, true);
+      if (elect()) {
+        if (ok) tc_commit(&S.o_full);
+        tc_commit(&S.mma_done);  // nothing in flight when TMEM is freed
+      }
+      __syncwarp();
+      __all_sync(0xffffffffu, wait_slow(&S.mma_done, 0, P.timeout_ns, S, true));
     }
   } else if (warp >= kHelper) {
     // ---- helpers: the tree, and V tiles that end the sequence ----
@@ -541,7 +561,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
     // back at the end).
 #pragma unroll 1
     for (int j = edge; j < T; ++j) {
-      const int x = 2 * j + 1, stage = x % Ge::kStages;
+      const int x = v_index(j, T), stage = x % Ge::kStages;
       if (!wait_count_warp(&S.v_issued, j - edge + 1, P, S)) break;
       if (!wait_warp(&S.full[stage], (x / Ge::kStages) & 1, P, S)) break;
       uint4* tile = reinterpret_cast<uint4*>(ring + stage * Ge::kTile);
@@ -575,66 +595,56 @@ __global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
       if (lane == 0) count_up(&S.v_clean);
     }
   } else {
-    // ---- softmax: two threads per row, one for each half of a tile's keys ----
+    // ---- softmax: one thread per row ----
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.q_full);
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_at = lane_base + w * kKeys + half * 64, o_at = lane_base + NT * kKeys + w * D + half * (D / 2);
-    const int node = first + w * P.nt + local;
+    const uint32_t s_at = lane_base, o_at = lane_base + 128;
+    const int node = first + local;
     const bool real = local < P.nt && node < nn;
     const bool any = __any_sync(0xffffffffu, real);  // else the warp's rows are left alone (their P is garbage)
     const uint32_t* anc = S.anc + (real ? node : 0) * kAncStride;
-    const int count = w == 0 || two ? T : 0;
-    // the row's other thread: tell it x, get its x (turn: a slot is written again two turns later)
-    auto tell = [&](float x, int turn) {
-      S.pair[turn & 1][half][w * kRows + row] = x;
-      named_bar_sync(1 + w * 4 + (warp & 3), 64);
-      return S.pair[turn & 1][half ^ 1][w * kRows + row];
-    };
     constexpr float kBias = FP16 ? 7.f : 0.f;
-    float m = -INFINITY, l = 0.f;  // maximum that P is taken against; sum of P over this thread's keys
-    bool ok = count == 0 || edge >= T || wait_warp(&S.anc_full, 0, P, S);
+    float m = -INFINITY, l = 0.f;  // maximum that P is taken against; sum of P
+    bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < count; ++j) {
-      ok = ok && wait_warp(&S.s_full[w], j & 1, P, S);
+    for (int j = 0; j < T; ++j) {
+      if (j == edge) ok = ok && wait_warp(&S.anc_full, 0, P, S);
+      ok = ok && wait_warp(&S.s_full[j & 1], (j >> 1) & 1, P, S);
       tc_fence_after();
       if (any) {
-        // a row of S is read twice, kCh keys at a time: for the maximum, and for the weights
-        const int rel = (t0 + j) * kKeys + half * 64 - len;  // > -64: drafts, or rows behind the last one
-        auto scores = [&](int k, uint32_t* s) {
-          tmem_ld32(s_at + k * kCh, s);
-          tmem_wait_ld();
-          tmem_use32(s);
-          if (rel + k * kCh > -kCh) {
-            const uint32_t see = visible32(anc, rel + k * kCh);
+        uint32_t s[kKeys];
+        tmem_ld32(s_at + (j & 1) * 64, s);
+        tmem_ld32(s_at + (j & 1) * 64 + 32, s + 32);
+        tmem_wait_ld();
+        tmem_use32(s);
+        tmem_use32(s + 32);
+        if (j >= edge) {  // the tile has drafts, or rows behind the last one
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t see = visible32(anc, (t0 + j) * kKeys + k * 32 - len);
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if (!(see >> x & 1)) s[x] = 0xff800000u;
-          }
-        };
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int k = 0; k < 64 / kCh; ++k) {
-          uint32_t s[kCh];
-          scores(k, s);
-#pragma unroll
-          for (int x = 0; x < kCh; x += 4) {
-            mx[0] = fmaxf(mx[0], fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
-            mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])));
+              if (!(see >> x & 1)) s[k * 32 + x] = 0xff800000u;
           }
         }
-        const float mine = fmaxf(mx[0], mx[1]);
-        const float top = fmaxf(fmaxf(mine, tell(mine, j)), m);
+        float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < kKeys; x += 2)
+          mx[x / 2 & 3] = fmaxf(mx[x / 2 & 3], fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const bool move = real && (top - m) * P.c > 8.f;  // also from -inf; false for -inf - -inf
         if (__any_sync(0xffffffffu, move)) {
           const float f = top == -INFINITY ? 1.f : ex2((m - top) * P.c);
           m = top;
           l *= f;
           if (j > 0) {
+            ok = ok && wait_warp(&S.o_done, (j - 1) & 1, P, S);  // (tile j - 2's is: S of tile j came after it)
+            tc_fence_after();
 #pragma unroll 1
-            for (int k = 0; k < D / 64; ++k) {
+            for (int k = 0; k < D / 32; ++k) {
               uint32_t o[32];
               tmem_ld32(o_at + k * 32, o);
               tmem_wait_ld();
@@ -646,42 +656,52 @@ __global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
           }
         }
         const float nm = m == -INFINITY ? 0.f : kBias - m * P.c;
-        float sum[2] = {0.f, 0.f};
-#pragma unroll 1
-        for (int k = 0; k < 64 / kCh; ++k) {
-          uint32_t s[kCh], p[kCh / 2];
-          scores(k, s);
+        const uint64_t nm2 = pack2(nm, nm), c2 = pack2(P.c, P.c);
+        uint64_t e[kKeys / 2];
 #pragma unroll
-          for (int x = 0; x < kCh / 2; ++x) {
-            float a0 = nm, a1 = nm;
-            fma2(a0, a1, __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), P.c, P.c);
-            a0 = ex2(a0), a1 = ex2(a1);
-            sum[0] += a0;
-            sum[1] += a1;
-            p[x] = pack16<FP16>(a0, a1);
-          }
-          tmem_st16(s_at + k * (kCh / 2), p);  // over scores that this thread has read
+        for (int x = 0; x < kKeys / 2; ++x) {
+          const uint64_t y = pack2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+          asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e[x]) : "l"(y), "l"(c2), "l"(nm2));
         }
-        l += sum[0] + sum[1];
+#pragma unroll
+        for (int x = 0; x < kKeys / 2; ++x) {
+          const float2 y = unpack2(e[x]);
+          e[x] = pack2(ex2(y.x), ex2(y.y));
+        }
+        uint64_t sum[4] = {e[0], e[1], e[2], e[3]};
+        uint32_t p[kKeys / 2];
+#pragma unroll
+        for (int x = 0; x < kKeys / 2; ++x) {
+          const float2 y = unpack2(e[x]);
+          p[x] = pack16<FP16>(y.x, y.y);
+          if (x >= 4) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[x & 3]) : "l"(e[x]));
+        }
+        tmem_st32(s_at + (j & 1) * 64, p);  // over scores that are read
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[0]) : "l"(sum[1]));
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[2]) : "l"(sum[3]));
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[0]) : "l"(sum[2]));
+        l += unpack2(sum[0]).x + unpack2(sum[0]).y;
         tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full[w]);
+      if (lane == 0) mbar_arrive(&S.p_full[j & 1]);
     }
     // ---- the end: every product is done, Q and the ring are read out ----
     if (T > 0) ok = ok && wait_warp(&S.o_full, 0, P, S);
     tc_fence_after();
-    if (C > 1) cluster_wait();
+    if (C > 1) {  // every block's Q and ring are read out
+      cluster_arrive();
+      cluster_wait();
+    }
     if (any) {
-      l += tell(l, count);
       if (C == 1) {
         if (ok) ok = wait_warp(&S.anc_full, 0, P, S);
         const float inv = l == 0.f || !real || !alive(S, node) ? 0.f : 1.f / l;
         uint16_t* out = P.o + (int64_t)b * P.o_seq + (int64_t)node * P.o_node +
-                        (int64_t)(h * P.G + row - local * P.G) * P.o_head + half * (D / 2);
+                        (int64_t)(h * P.G + row - local * P.G) * P.o_head;
 #pragma unroll 1
-        for (int k = 0; k < D / 64; ++k) {
+        for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
           tmem_ld32(o_at + k * 32, o);
           tmem_wait_ld();
@@ -698,27 +718,38 @@ __global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
               *reinterpret_cast<uint4*>(out + k * 32 + x) = make_uint4(p[0], p[1], p[2], p[3]);
             }
         }
-        if (S.bad_v && real) add_nonfinite<FP16>(P, S, b, h, len, node, half * (D / 2), D / 2, out);
+        if (S.bad_v && real) add_nonfinite<FP16>(P, S, b, h, len, node, 0, D, out);
       } else {
-        // this block's partial result: O over Q's and the ring's room, and each row's statistics to
-        // the block that finishes the row
-        if (real && half == 0) {
-          const int r = w * P.nt * P.G + row, owner = r / per;
-          st_peer_f2(mapa(smem_u32(&S.stat[(r - owner * per) * C + rank]), owner), m, l);
+        // a row's statistics and O to the block that finishes it, over that block's Q and ring
+        const int owner = real ? row / per : 0, x = row - owner * per;
+        if (real) {
+          st_peer_f2(mapa(smem_u32(&S.stat[x * C + rank]), owner), m, l);
           if (S.bad_v) st_peer_u32(mapa(smem_u32(&S.bad_any), owner), 1);
         }
-        if (count > 0) {
-          float* dst = reinterpret_cast<float*>(data) + (size_t)(w * kRows + row) * Ge::kOStride + half * (D / 2);
+        if (T > 0) {
+          // 32 columns at a time through a corner of shared memory, so that a row's 128 bytes leave
+          // together: eight lanes per row
+          const uint32_t dst = mapa(smem_u32(data) + (uint32_t)((rank * per + x) * Ge::kOStride * 4), owner);
+          float* corner = reinterpret_cast<float*>(data + Ge::kStageAt) + warp * 32 * Ge::kStageStride;
+          const int rows_here = min(32, rows - warp * 32);
 #pragma unroll 1
-          for (int k = 0; k < D / 64; ++k) {
+          for (int k = 0; k < D / 32; ++k) {
             uint32_t o[32];
             tmem_ld32(o_at + k * 32, o);
             tmem_wait_ld();
             tmem_use32(o);
-            if (real)
 #pragma unroll
-              for (int x = 0; x < 32; x += 4)
-                *reinterpret_cast<uint4*>(dst + k * 32 + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            for (int y = 0; y < 32; y += 4)
+              *reinterpret_cast<uint4*>(corner + lane * Ge::kStageStride + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            __syncwarp();
+#pragma unroll 2
+            for (int y = 0; y < rows_here; y += 4) {
+              const int from = y + lane / 8;
+              const uint32_t to = __shfl_sync(0xffffffffu, dst, from & 31);
+              const uint4 v = *reinterpret_cast<const uint4*>(corner + from * Ge::kStageStride + lane % 8 * 4);
+              if (from < rows_here) st_peer_v4(to + (k * 32 + lane % 8 * 4) * 4, v);
+            }
+            __syncwarp();
           }
         }
       }
@@ -727,73 +758,90 @@ __global__ void __launch_bounds__(Geo<D, NT>::kThreads, 3 - NT)
   }
   __syncwarp();
   if (C > 1) {
-    if (warp >= Ge::kSoft) cluster_wait();
-    cluster_arrive();
+    if (warp >= kSoft) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    cluster_arrive();  // every partial result has arrived; no block touches another's memory after this
     cluster_wait();
   } else {
     __syncthreads();
   }
   tc_fence_after();
   if (warp == kMmaWarp) tc_dealloc(tmem, Ge::kCols);
-  if (C > 1) {
-    if (on) merge<D, FP16, NT>(P, S, data, b, h, first, rows, per, rank, C, len, warp, lane);
-    __syncwarp();
-    cluster_arrive();  // peers read this block's shared memory until here
-    cluster_wait();
-  }
+  if (C > 1 && on)
+    merge<D, FP16>(P, S, reinterpret_cast<const float*>(data), b, h, first, rows, per, rank, C, len, warp, lane);
 }
 
-template <int D, bool FP16, int NT>
-static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, const Params& P, int64_t units, int n_sms,
-                          cudaStream_t stream) {
-  constexpr int kSmem = Geo<D, NT>::kData + 1024;
-  const auto kernel = tree_attention<D, FP16, NT>;
-  // the largest cluster that fits the device, found once per device: 16, or the portable 8
-  static std::atomic<int> largest[64];
+// Clusters of 2, 4, 8 and 16 blocks that the device runs at once, asked once per device and kernel.
+// (The query counts one block per SM for this kernel at any size of shared memory; two run, by
+// their active warps, so its answer is doubled.)
+template <int D, bool FP16>
+static cudaError_t clusters_at_once(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int* fit) {
+  static std::atomic<uint64_t> known[64];  // four counts of 16 bits, 1 + each
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  uint64_t v = dev < 64 ? known[dev].load() : 0;
+  if (!v) {
+    const auto kernel = tree_attention<D, FP16>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)  // two blocks per SM need nearly all of its shared memory
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    for (int k = 0; k < 4; ++k) {
+      attr[0].val.clusterDim.x = 2u << k;
+      cfg.gridDim = dim3(2u << k);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      v |= (uint64_t)(1 + (n < 60000 ? n : 60000)) << (16 * k);
+    }
+    if (dev < 64) known[dev].store(v);
+  }
+  for (int k = 0; k < 4; ++k) fit[k] = 2 * ((int)(v >> (16 * k) & 0xffff) - 1);
+  return cudaSuccess;
+}
+
+template <int D, bool FP16>
+static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params& P, int B, int n_sms, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(Geo<D, NT>::kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Geo<D>::kData + 1024;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int most = dev < 64 ? largest[dev].load() : 0;
-  if (!most) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    attr[0].val.clusterDim.x = kMaxCluster;
-    cfg.gridDim = dim3(kMaxCluster);
-    int fit = 0;
-    if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      fit = 0;
-    }
-    most = fit >= 1 ? kMaxCluster : 8;
-    if (dev < 64) largest[dev].store(most);
-  }
-  // Keys are split while that gives idle SMs work, down to one tile per block.
+  int fit[4];
+  const cudaError_t e = clusters_at_once<D, FP16>(cfg, attr, fit);
+  if (e != cudaSuccess) return e;
+  P.units = (P.n + P.nt - 1) / P.nt;
+  const int64_t units = (int64_t)B * P.hkv * P.units;
+  if (units > (1 << 27)) return cudaErrorInvalidValue;
+  // Blocks that share a unit's keys: the split with the least estimated time.  A block takes as long
+  // as 8 tiles for its start and end, and half as long again where two share an SM; more clusters
+  // than run at once go in turns (a few more than one turn's cost little).  Measured, us for 1, 2, 4,
+  // 8, 16 blocks: 8 units of 4122 rows 53 35 25 19 18; 16 units of 2056 rows 31 23 17 14 23; 64 units
+  // of 16448 rows 192 107 82 110 150; 512 units of 4352 rows 136 147 180 270 577.
+  const double tiles = (double)P.max_seq / kKeys;
   int C = 1;
-  while (2 * C <= most && units * 2 * C <= n_sms && (int64_t)C * kKeys < P.max_seq) C *= 2;
+  double best = 0.0;
+  for (int k = 0; k < 5 && (k == 0 || (int64_t)kKeys << (k - 1) < P.max_seq); ++k) {
+    const int at_once = k == 0 ? 2 * n_sms : fit[k - 1];
+    if (at_once < 1) continue;
+    const double turns = (double)units / at_once;
+    const double t = (8.0 + tiles / (1 << k)) * (units << k > n_sms ? 1.5 : 1.0) *
+                     (turns <= 1.0 ? 1.0 : turns <= 1.1 ? turns : ceil(turns));
+    if (k == 0 || t < best) best = t, C = 1 << k;
+  }
   attr[0].val.clusterDim.x = C;
   cfg.gridDim = dim3((unsigned)(units * C));
-  return cudaLaunchKernelEx(&cfg, kernel, mk_, mv, P);
-}
-
-template <int D, bool FP16>
-static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params& P, int B, int n_sms,
-                          cudaStream_t stream) {
-  const int tiles = (P.n + P.nt - 1) / P.nt, NT = tiles > 1 ? 2 : 1;
-  P.units = (tiles + NT - 1) / NT;
-  const int64_t units = (int64_t)B * P.hkv * P.units;
-  if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  return NT == 2 ? launch<D, FP16, 2>(mk_, mv, P, units, n_sms, stream)
-                 : launch<D, FP16, 1>(mk_, mv, P, units, n_sms, stream);
+  return cudaLaunchKernelEx(&cfg, tree_attention<D, FP16>, mk_, mv, P);
 }
 
 static bool encode(CUtensorMap* map, const void* base, int fp16, int D, int max_seq, int hkv, int B, int64_t seq,

@@ -384,7 +384,8 @@ int mk_attention_debug_drop_unit(int unit);
 /* Sizes and element strides of a tree attention.  The last axis (head_dim values) is contiguous;
  * every stride is a multiple of 8 elements (the stride of an axis of length 1 is not used). */
 typedef struct mk_tree_shape {
-  int dtype; /* MK_BF16 or MK_FP16: q, k, v and o */
+  int dtype; /* MK_BF16 or MK_FP16: k and v, and q and o unless wide */
+  int wide;  /* 1: q and o are fp32, and no step is rounded to fewer than 16 (fp16: 22) bits; 0: not */
   int B, n, n_q_heads, n_kv_heads, head_dim, max_seq;
   int64_t q_seq, q_node, q_head; /* q[b][i][h][..] */
   int64_t k_seq, k_head, k_row;  /* k[b][h][row][..], 0 <= row < max_seq */
@@ -396,8 +397,8 @@ typedef struct mk_tree_shape {
  *   o[b][i][h] = sum_j softmax_j(scale * q[b][i][h] . k[b][h / G][j]) v[b][h / G][j],
  *   j in {0 .. lens[b] - 1} and lens[b] + a for a = i, parents[b][i], its parent, ..
  * with G = n_q_heads / n_kv_heads.  n = 1 is decode attention over lens[b] + 1 rows.  Softmax and
- * sums in fp32; the softmax weights are rounded to the inputs' type for the product with v.  k and
- * v: one layer of the decoder's cache, or any such arrays.  Rows that a node does not see have no
+ * sums in fp32; the softmax weights are rounded to the inputs' type for the product with v (wide: as
+ * the sum of two such values; fp32 q for an fp16 cache is within fp16's range).  k and v: one layer of the decoder's cache, or any such arrays.  Rows that a node does not see have no
  * influence on it, whatever they hold; infinities and NaN in rows that it sees reach its output.
  * A node whose parents are not a tree's (parents[b][i] outside [-1, i), or such an ancestor) gets
  * zeros.  Requirements: head_dim 64 or 128; n_q_heads % n_kv_heads == 0, G <= 128; 1 <= n <=
@@ -411,6 +412,17 @@ int mk_tree_attention(const mk_tree_shape* shape, const void* q, const void* k, 
  * output is undefined; cleared by this call) or not (MK_OK).  The limit of the waits is
  * mk_attention_set_wait_timeout_ns's. */
 int mk_tree_attention_status(void* stream);
+
+/* The target model's logits after every node, on the prompt kernels with mk_tree_attention (wide) in
+ * each layer: as exact as mk_prefill.  tokens: device int32 [B][n];
+ * lens: the rows of each sequence in kv_cache, which here are its positions too.  Node i of sequence
+ * b stands at position lens[b] + the number of its ancestors; its keys and values are written to
+ * cache row lens[b] + i of every layer, for mk_cache_commit to keep or the next call to overwrite.
+ * logits: device fp32 [B][n][vocab]; rows of nodes not in use are undefined.  B <= max_batch, B * n
+ * <= min(1024, max_batch * max_seq).  The context's own positions are neither read nor changed: before
+ * a decode step set them (mk_set_positions) to the lengths that mk_cache_commit left. */
+int mk_tree_forward(mk_ctx* ctx, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                    const int32_t* lens, int B, int n, void* kv_cache, float* logits, void* stream);
 
 /* Sizes and element strides of a verification; the last axis (vocab logits) is contiguous. */
 typedef struct mk_verify_shape {

@@ -77,7 +77,7 @@ class mk_graph_info(ctypes.Structure):
 
 
 class mk_tree_shape(ctypes.Structure):
-    _fields_ = [(name, ctypes.c_int) for name in ("dtype", "B", "n", "n_q_heads", "n_kv_heads", "head_dim",
+    _fields_ = [(name, ctypes.c_int) for name in ("dtype", "wide", "B", "n", "n_q_heads", "n_kv_heads", "head_dim",
                                                   "max_seq")] + \
         [(name, ctypes.c_int64) for name in ("q_seq", "q_node", "q_head", "k_seq", "k_head", "k_row",
                                              "v_seq", "v_head", "v_row", "o_seq", "o_node", "o_head")]
@@ -130,6 +130,7 @@ _SIGS = {
     "mk_tree_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp],
                           _i32),
     "mk_tree_attention_status": ([_vp], _i32),
+    "mk_tree_forward": ([_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp], _i32),
     "mk_tree_verify_workspace_bytes": ([_i32, _i32, _i32], _sz),
     "mk_tree_verify": ([_vp] * 15, _i32),
     "mk_cache_commit": ([_vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp], _i32),
@@ -391,7 +392,7 @@ def mk_attention_debug_drop_unit(unit: int):
 # A decoding loop makes these calls for kernels of a few microseconds, so the checks are kept
 # cheap: plain comparisons, and the shape structs packed instead of built field by field.
 
-_TREE_SHAPE = struct.Struct("7i4x12q")
+_TREE_SHAPE = struct.Struct("8i12q")
 _VERIFY_SHAPE = struct.Struct("4i4q")
 _CACHE_SHAPE = struct.Struct("6i")
 _types = None  # (torch, {dtype: code}): torch is only imported by the calls that take tensors
@@ -440,7 +441,7 @@ def _call(torch, f, tensors, *args):
 def mk_tree_attention(q, k, v, o, parents, n_nodes, lens, scale: float, stream=None):
     """Attention of drafted trees over a cache.  q, o: [B, n, n_q_heads, head_dim]; k, v: [B,
     n_kv_heads, max_seq, head_dim] (e.g. ``kv_view()[layer, 0]`` and ``[layer, 1]``); bf16 or
-    fp16, any strides with a contiguous last axis; parents [B, n], lens [B] and n_nodes [B] (or
+    fp16 (q and o also fp32), any strides with a contiguous last axis; parents [B, n], lens [B] and n_nodes [B] (or
     None) int32."""
     torch, codes = _types or _torch_types()
     if q.dim() != 4 or k.dim() != 4 or o.shape != q.shape or v.shape != k.shape:
@@ -449,9 +450,11 @@ def mk_tree_attention(q, k, v, o, parents, n_nodes, lens, scale: float, stream=N
     kB, hkv, S, kd = k.shape
     if kB != B or kd != d:
         _refuse("q and k differ in batch or head_dim")
-    code = codes.get(q.dtype)
-    if code is None or not (code == codes.get(k.dtype) == codes.get(v.dtype) == codes.get(o.dtype)):
-        _refuse("q, k, v and o must have one type: bfloat16 (or its bits as int16) or float16")
+    code, qc = codes.get(k.dtype), codes.get(q.dtype)
+    wide = qc == MK_FP32
+    if code not in (MK_BF16, MK_FP16) or code != codes.get(v.dtype) or qc != codes.get(o.dtype) or \
+            not (wide or qc == code):
+        _refuse("k and v must be bfloat16 (or its bits as int16) or float16; q and o the same, or float32")
     q0, q1, q2, q3 = q.stride()
     k0, k1, k2, k3 = k.stride()
     v0, v1, v2, v3 = v.stride()
@@ -460,7 +463,7 @@ def mk_tree_attention(q, k, v, o, parents, n_nodes, lens, scale: float, stream=N
         _refuse("the last axis of q, k, v and o must be contiguous")
     i32 = torch.int32
     _call(torch, _lib.mk_tree_attention, (q, k, v, o, parents, lens, n_nodes),
-          _TREE_SHAPE.pack(code, B, n, hq, hkv, d, S, q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2),
+          _TREE_SHAPE.pack(code, wide, B, n, hq, hkv, d, S, q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2),
           q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _index(parents, (B, n), i32, "parents"),
           _index(n_nodes, (B,), i32, "n_nodes"), _index(lens, (B,), i32, "lens"), scale, _stream(stream))
 
@@ -469,6 +472,12 @@ def mk_tree_attention_status(stream=None) -> int:
     """MK_OK, or MK_ERR_DEVICE_TIMEOUT if a tree attention since the last status call had a device
     wait run out (returned, not raised)."""
     return _lib.mk_tree_attention_status(_stream(stream))
+
+
+def mk_tree_forward(ctx, tokens, parents, n_nodes, lens, B: int, n: int, kv_cache, logits, stream=None):
+    """The target model's logits after every node of B drafted trees; see include/mk.h."""
+    _check(_lib.mk_tree_forward(ctx, _ptr(tokens), _ptr(parents), _ptr(n_nodes), _ptr(lens), int(B), int(n),
+                                _ptr(kv_cache), _ptr(logits), _stream(stream)), ctx)
 
 
 def mk_tree_verify_workspace_bytes(B: int, n: int, vocab: int) -> int:
@@ -630,6 +639,35 @@ class Megakernel:
         out = torch.empty((n_steps, self.cfg.max_batch), dtype=torch.int32, device=tokens.device)
         mk_decode_steps(self.ctx, tokens, n_steps, self.kv, self.logits, out, self.stream)
         return self.logits[:B], out[:, :B]
+
+    def tree_forward(self, tokens, parents, lens, n_nodes=None):
+        """Logits [B, n, vocab] after every node of drafted trees (tokens, parents: int32 CUDA [B, n];
+        lens: int32 CUDA [B], the rows of each sequence in the cache, all of them known to the
+        device: the positions kept by the context are not used).  Node 0 is the last token."""
+        import torch
+        B, n = tokens.shape
+        i32 = torch.int32
+        for t, shape, what in ((tokens, (B, n), "tokens"), (parents, (B, n), "parents"), (lens, (B,), "lens"),
+                               (n_nodes, (B,), "n_nodes")):
+            _index(t, shape, i32, what)
+        out = torch.empty((B, n, self.cfg.vocab), dtype=torch.float32, device=tokens.device)
+        mk_tree_forward(self.ctx, tokens, parents, n_nodes, lens, B, n, self.kv, out, self.stream)
+        return out
+
+    def commit(self, path, n_path, lens):
+        """Keep the accepted nodes (as mk_tree_verify leaves path and n_path) of the trees last
+        forwarded; returns the new lengths (int32 CUDA [B])."""
+        import torch
+        new_lens = torch.empty_like(lens)
+        mk_cache_commit(self.kv_view(), path, n_path, lens, new_lens, self.stream)
+        return new_lens
+
+    def reorder(self, src, lens):
+        """Sequence b takes over sequence src[b]'s cache rows; returns the new lengths."""
+        import torch
+        new_lens = torch.empty_like(lens)
+        mk_cache_reorder(self.kv_view(), src, lens, new_lens, self.stream)
+        return new_lens
 
     def calibrate(self, tokens, steps: int = 2, rounds: int = 3):
         """Measure each SM's busy time on each projection (QKV, O, gate/up, down, LM head) over

@@ -1596,14 +1596,7 @@ int mk_load_weights(mk_ctx* c, const mk_host_weights* w, void* weight_arena, voi
   return MK_OK;
 }
 
-int mk_prefill(mk_ctx* c, const int32_t* tokens, int B, int T, void* kv_cache, float* last_logits, void* stream) {
-  if (!c) return fail(nullptr, MK_ERR_INVALID_ARG, "ctx is NULL");
-  if (!c->tp_shards.empty())
-    return fail(c, MK_ERR_UNSUPPORTED, "tensor-parallel contexts take the prompt as decode steps (or a filled cache)");
-  if (!c->loaded) return fail(c, MK_ERR_STATE, "weights not loaded");
-  if (!tokens || !kv_cache) return fail(c, MK_ERR_INVALID_ARG, "NULL tokens or cache");
-  if (B < 1 || B > c->cfg.max_batch || T < 1 || T > c->cfg.max_seq)
-    return fail(c, MK_ERR_INVALID_ARG, "B or T out of range");
+static PrefillParams prefill_params(mk_ctx* c, void* kv_cache) {
   const mk_config& f = c->cfg;
   PrefillParams p;
   p.arena = c->arena;
@@ -1638,11 +1631,40 @@ int mk_prefill(mk_ctx* c, const int32_t* tokens, int B, int T, void* kv_cache, f
   p.ndc = c->ndc;
   p.blocked = c->tc ? 1 : 0;
   p.qk_norm = f.qk_norm;
+  return p;
+}
+
+int mk_prefill(mk_ctx* c, const int32_t* tokens, int B, int T, void* kv_cache, float* last_logits, void* stream) {
+  if (!c) return fail(nullptr, MK_ERR_INVALID_ARG, "ctx is NULL");
+  if (!c->tp_shards.empty())
+    return fail(c, MK_ERR_UNSUPPORTED, "tensor-parallel contexts take the prompt as decode steps (or a filled cache)");
+  if (!c->loaded) return fail(c, MK_ERR_STATE, "weights not loaded");
+  if (!tokens || !kv_cache) return fail(c, MK_ERR_INVALID_ARG, "NULL tokens or cache");
+  if (B < 1 || B > c->cfg.max_batch || T < 1 || T > c->cfg.max_seq)
+    return fail(c, MK_ERR_INVALID_ARG, "B or T out of range");
+  const PrefillParams p = prefill_params(c, kv_cache);
   std::string err;
   int rc = run_prefill(p, tokens, B, T, last_logits, reinterpret_cast<cudaStream_t>(stream), &err);
   if (rc) return fail(c, rc, err);
   c->B = B;
   for (int b = 0; b < B; ++b) c->pos[b] = T;
+  return MK_OK;
+}
+
+int mk_tree_forward(mk_ctx* c, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                    const int32_t* lens, int B, int n, void* kv_cache, float* logits, void* stream) {
+  if (!c) return fail(nullptr, MK_ERR_INVALID_ARG, "ctx is NULL");
+  if (!c->tp_shards.empty()) return fail(c, MK_ERR_UNSUPPORTED, "tensor-parallel contexts have no tree forward");
+  if (!c->loaded) return fail(c, MK_ERR_STATE, "weights not loaded");
+  if (!tokens || !parents || !lens || !kv_cache || !logits) return fail(c, MK_ERR_INVALID_ARG, "NULL operand");
+  if (B < 1 || B > c->cfg.max_batch || n < 1 || n > MK_MAX_TREE_NODES)
+    return fail(c, MK_ERR_INVALID_ARG, "B or n out of range");
+  if (B * n > c->pf_rows)
+    return fail(c, MK_ERR_INVALID_ARG, "B * n exceeds the prefill scratch (" + std::to_string(c->pf_rows) + " rows)");
+  std::string err;
+  const int rc = run_tree_forward(prefill_params(c, kv_cache), tokens, parents, n_nodes, lens, B, n, logits, c->n_sms,
+                                  reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(c, rc, err);
   return MK_OK;
 }
 
@@ -2081,6 +2103,7 @@ int mk_tree_attention(const mk_tree_shape* shape, const void* q, const void* k, 
   mk_tree_shape s = *shape;
   if (s.dtype != MK_BF16 && s.dtype != MK_FP16)
     return fail(nullptr, MK_ERR_INVALID_ARG, "tree attention takes MK_BF16 or MK_FP16");
+  if (s.wide != 0 && s.wide != 1) return fail(nullptr, MK_ERR_INVALID_ARG, "wide must be 0 or 1");
   if (s.B < 1 || s.n < 1 || s.n > MK_MAX_TREE_NODES || s.max_seq < 1 || (s.head_dim != 64 && s.head_dim != 128))
     return fail(nullptr, MK_ERR_INVALID_ARG, "bad B, n, max_seq or head_dim");
   if (s.n_kv_heads < 1 || s.n_q_heads < 1 || s.n_q_heads % s.n_kv_heads || s.n_q_heads / s.n_kv_heads > 128)

@@ -260,5 +260,7 @@ struct PrefillParams {
 };
 int run_prefill(const PrefillParams& p, const int32_t* tokens, int B, int T, float* last_logits,
                 cudaStream_t stream, std::string* err);
+int run_tree_forward(const PrefillParams& p, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                     const int32_t* lens, int B, int n, float* logits, int n_sms, cudaStream_t s, std::string* err);
 
 }  // namespace mk

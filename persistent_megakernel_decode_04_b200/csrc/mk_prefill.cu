@@ -176,6 +176,51 @@ __global__ void qkv_post(const float* Yq, int n, int ct, int t0, const float2* r
   }
 }
 
+// The same for row (b, i) of a step over drafted trees: node i of sequence b.  It is rotated to
+// position lens[b] + depth (its ancestors' count), and its K and V go to cache row lens[b] + i.
+// Nodes that do not fit the cache write nothing to it.
+__global__ void tree_qkv_post(const float* Yq, int n, const int32_t* parents, const int32_t* lens, const float2* rope,
+                              float* Q, uint16_t* kv, int layer, int nq, int nkv, int D, int max_seq,
+                              int max_batch) {
+  __shared__ int s_pos;
+  const int row = blockIdx.x, b = row / n, i = row % n;
+  const int len = min(max(lens[b], 0), max_seq), at = len + i;
+  if (threadIdx.x == 0) {
+    int depth = 0;
+    for (int c = i; depth < i; ++depth) {
+      const int up = parents[(size_t)b * n + c];
+      if (up < 0 || up >= c) break;  // a root; or not a tree's: the node's results are not used
+      c = up;
+    }
+    s_pos = min(len + depth, max_seq - 1);
+  }
+  __syncthreads();
+  const int pos = s_pos;
+  const int G = nq / nkv, half = D / 2, rpg = (G + 2) * D, NQKV = (nq + 2 * nkv) * D;
+  const size_t head_stride = (size_t)max_seq * D;
+  const size_t kv_layer = (size_t)max_batch * nkv * head_stride;
+  const float* y = Yq + (size_t)row * NQKV;
+  for (int R = threadIdx.x; R < NQKV; R += blockDim.x) {
+    const int grp = R / rpg, rr = R % rpg;
+    const float v = y[R];
+    const size_t cell = ((size_t)b * nkv + grp) * head_stride + (size_t)at * D;
+    if (rr < (G + 1) * D) {
+      const int pd = (rr < G * D) ? (rr % D) : (rr - G * D);
+      const int k = pd >> 1, hi = pd & 1;
+      const float other = y[R ^ 1];
+      const float2 cs = rope[(size_t)pos * half + k];
+      const float outv = hi ? (v * cs.x + other * cs.y) : (v * cs.x - other * cs.y);
+      const int dim = hi ? k + half : k;
+      if (rr < G * D)
+        Q[(size_t)row * nq * D + (size_t)(grp * G + rr / D) * D + dim] = outv;
+      else if (at < max_seq)
+        kv[((size_t)layer * 2 + 0) * kv_layer + cell + dim] = f2bf(outv);
+    } else if (at < max_seq) {
+      kv[((size_t)layer * 2 + 1) * kv_layer + cell + rr - (G + 1) * D] = f2bf(v);
+    }
+  }
+}
+
 // Causal attention of chunk row (b, pos) and query head h over cache positions 0..pos.
 // One block per (row, head); scores staged in dynamic shared memory (pos + 1 floats).
 __global__ void __launch_bounds__(128) attention(const float* Q, const uint16_t* kv, float* O, int ct, int t0,
@@ -263,9 +308,25 @@ static void gemm(const float* A, const uint16_t* W, float* Y, int n, int N, int 
   pf::gemm<<<grid, 256, 0, s>>>(A, W, Y, n, N, K, lda < 0 ? K : lda, ldy, accumulate, blocked);
 }
 
+// A layer from the attention's output p.O on: O projection, residual, norm, SwiGLU MLP, residual.
+static void after_attention(const PrefillParams& p, const LayerOff& lo, int n, cudaStream_t s) {
+  const int H = p.H, F = p.F;
+  const uint16_t* mn = reinterpret_cast<const uint16_t*>(p.arena + lo.mlp_norm);
+  gemm(p.O, reinterpret_cast<const uint16_t*>(p.arena + lo.o), p.Y, n, H, p.nq * p.D, H, s, p.blocked);
+  pf::residual_add<<<256, 256, 0, s>>>(p.X, p.Y, (size_t)n * H);
+  pf::rmsnorm<<<n, 256, 0, s>>>(p.X, mn, p.XN, H, p.eps, 1, 0);
+  gemm(p.XN, reinterpret_cast<const uint16_t*>(p.arena + lo.gu), p.Y, n, 2 * F, H, 2 * F, s, p.blocked);
+  pf::swiglu<<<n, 256, 0, s>>>(p.Y, p.HH, F);
+  for (int k = 0; k < p.ndc; ++k) {  // W_down in chunk-major K chunks (one chunk when unsplit)
+    const int k0 = k * p.kdc, kc = (F - k0) < p.kdc ? (F - k0) : p.kdc;
+    gemm(p.HH + k0, reinterpret_cast<const uint16_t*>(p.arena + lo.d) + (size_t)H * k0, p.Y, n, H, kc, H, s, p.blocked, F, k);
+  }
+  pf::residual_add<<<256, 256, 0, s>>>(p.X, p.Y, (size_t)n * H);
+}
+
 int run_prefill(const PrefillParams& p, const int32_t* tokens, int B, int T, float* last_logits, cudaStream_t s,
                 std::string* err) {
-  const int H = p.H, D = p.D, F = p.F, nq = p.nq, nkv = p.nkv;
+  const int H = p.H, D = p.D, nq = p.nq, nkv = p.nkv;
   const int NQKV = (nq + 2 * nkv) * D;
   const int ct_max = p.rows_cap / B;
   if (ct_max < 1) {
@@ -283,7 +344,6 @@ int run_prefill(const PrefillParams& p, const int32_t* tokens, int B, int T, flo
     for (int l = 0; l < p.L; ++l) {
       const LayerOff& lo = p.loff_host[l];
       const uint16_t* an = reinterpret_cast<const uint16_t*>(p.arena + lo.attn_norm);
-      const uint16_t* mn = reinterpret_cast<const uint16_t*>(p.arena + lo.mlp_norm);
       pf::rmsnorm<<<n, 256, 0, s>>>(p.X, an, p.XN, H, p.eps, 1, 0);
       gemm(p.XN, reinterpret_cast<const uint16_t*>(p.arena + lo.qkv), p.Y, n, NQKV, H, NQKV, s, p.blocked);
       if (p.qk_norm)
@@ -293,16 +353,7 @@ int run_prefill(const PrefillParams& p, const int32_t* tokens, int B, int T, flo
       if (smem > 48 * 1024) cudaFuncSetAttribute(pf::attention, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       pf::attention<<<n * nq, 128, smem, s>>>(p.Q, p.kv, p.O, ct, t0, l, nq, nkv, D, p.max_seq, p.max_batch,
                                               p.attn_scale);
-      gemm(p.O, reinterpret_cast<const uint16_t*>(p.arena + lo.o), p.Y, n, H, nq * D, H, s, p.blocked);
-      pf::residual_add<<<256, 256, 0, s>>>(p.X, p.Y, (size_t)n * H);
-      pf::rmsnorm<<<n, 256, 0, s>>>(p.X, mn, p.XN, H, p.eps, 1, 0);
-      gemm(p.XN, reinterpret_cast<const uint16_t*>(p.arena + lo.gu), p.Y, n, 2 * F, H, 2 * F, s, p.blocked);
-      pf::swiglu<<<n, 256, 0, s>>>(p.Y, p.HH, F);
-      for (int k = 0; k < p.ndc; ++k) {  // W_down in chunk-major K chunks (one chunk when unsplit)
-        const int k0 = k * p.kdc, kc = (F - k0) < p.kdc ? (F - k0) : p.kdc;
-        gemm(p.HH + k0, reinterpret_cast<const uint16_t*>(p.arena + lo.d) + (size_t)H * k0, p.Y, n, H, kc, H, s, p.blocked, F, k);
-      }
-      pf::residual_add<<<256, 256, 0, s>>>(p.X, p.Y, (size_t)n * H);
+      after_attention(p, lo, n, s);
     }
     if (!ck(cudaGetLastError(), "prefill chunk", err)) return MK_ERR_CUDA;
   }
@@ -314,6 +365,40 @@ int run_prefill(const PrefillParams& p, const int32_t* tokens, int B, int T, flo
   }
   (void)last_t0;
   if (!ck(cudaGetLastError(), "prefill", err)) return MK_ERR_CUDA;
+  return MK_OK;
+}
+
+// One pass of the model over drafted trees: prompt kernels around the tree attention.
+int run_tree_forward(const PrefillParams& p, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                     const int32_t* lens, int B, int n, float* logits, int n_sms, cudaStream_t s, std::string* err) {
+  const int H = p.H, D = p.D, nq = p.nq, nkv = p.nkv, rows = B * n;
+  const int NQKV = (nq + 2 * nkv) * D;
+  mk_tree_shape t = {};
+  t.dtype = MK_BF16, t.wide = 1;
+  t.B = B, t.n = n, t.n_q_heads = nq, t.n_kv_heads = nkv, t.head_dim = D, t.max_seq = p.max_seq;
+  t.q_head = t.o_head = D;
+  t.q_node = t.o_node = (int64_t)nq * D;
+  t.q_seq = t.o_seq = t.q_node * n;
+  t.k_row = t.v_row = D;
+  t.k_head = t.v_head = (int64_t)p.max_seq * D;
+  t.k_seq = t.v_seq = t.k_head * nkv;
+  const size_t plane = (size_t)p.max_batch * nkv * p.max_seq * D;
+  pf::embed<<<rows, 256, 0, s>>>(tokens, n, 0, n, reinterpret_cast<const uint16_t*>(p.arena + p.off_embed), p.X, H, p.V);
+  for (int l = 0; l < p.L; ++l) {
+    const LayerOff& lo = p.loff_host[l];
+    pf::rmsnorm<<<rows, 256, 0, s>>>(p.X, reinterpret_cast<const uint16_t*>(p.arena + lo.attn_norm), p.XN, H, p.eps, 1, 0);
+    gemm(p.XN, reinterpret_cast<const uint16_t*>(p.arena + lo.qkv), p.Y, rows, NQKV, H, NQKV, s, p.blocked);
+    if (p.qk_norm)
+      pf::qk_norm<<<rows, 256, 0, s>>>(p.Y, reinterpret_cast<const uint16_t*>(p.arena + lo.qkn), nq, nkv, D, p.eps);
+    pf::tree_qkv_post<<<rows, 256, 0, s>>>(p.Y, n, parents, lens, p.rope, p.Q, p.kv, l, nq, nkv, D, p.max_seq, p.max_batch);
+    const int rc = tree_attention(t, p.Q, p.kv + 2 * l * plane, p.kv + (2 * l + 1) * plane, p.O, parents, n_nodes, lens,
+                                  p.attn_scale, n_sms, s, err);
+    if (rc) return rc;
+    after_attention(p, lo, rows, s);
+  }
+  pf::rmsnorm<<<rows, 256, 0, s>>>(p.X, reinterpret_cast<const uint16_t*>(p.arena + p.off_fnorm), p.XN, H, p.eps, 1, 0);
+  gemm(p.XN, reinterpret_cast<const uint16_t*>(p.arena + p.off_lm), logits, rows, p.V, H, p.V, s, p.blocked);
+  if (!ck(cudaGetLastError(), "tree forward", err)) return MK_ERR_CUDA;
   return MK_OK;
 }
 

@@ -24,13 +24,16 @@
 // Precision.  S, the softmax statistics and O are fp32.  P is rounded to the inputs' 16-bit type
 // for the second product (relative 2^-9 / 2^-12, the size of the output's own rounding).  The
 // maximum that P is taken against is only moved when it grows by more than 2^8; fp16 takes P
-// times 2^7, so that small weights stay clear of fp16's subnormals (largest 2^15).
+// times 2^7, so that small weights stay clear of fp16's subnormals (largest 2^15).  With fp32 q and o
+// (WIDE) q and P each enter their product as two 16-bit parts, the value's rounding and what that
+// left over, so that both products see 16 (bf16) or 22 (fp16) bits of them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mk_internal.h"
 #include "mk_ptx.cuh"
@@ -48,28 +51,29 @@ constexpr int kSoft = 4;          // softmax warps; then loads, products, two he
 constexpr int kTmaWarp = 4, kMmaWarp = 5, kHelper = 6;
 constexpr int kThreads = 256;
 
-template <int D>
+template <int D, bool WIDE>
 struct Geo {
   static constexpr int kTile = kKeys * D * 2;      // bytes of a K or V tile
   static constexpr int kQTile = kRows * D * 2;
   static constexpr int kStages = 4 * (128 / D);
-  static constexpr int kData = kQTile + kStages * kTile;
+  static constexpr int kQ = kQTile * (WIDE ? 2 : 1);  // high parts, then low parts
+  static constexpr int kData = kQ + kStages * kTile;
   static constexpr int kOStride = D + 4;           // floats: 16-byte rows, no bank conflicts
   // Behind the partial O's (over Q and the ring): a warp's 32 rows x 32 columns on their way out
   static constexpr int kStageStride = 36;
   static constexpr int kStageAt = (kRows + kMaxCluster) * kOStride * 4;
   static_assert(kStageAt + kSoft * 32 * kStageStride * 4 <= kData, "partial O's and stages fit over Q and the ring");
-  // Tensor memory: S of even and odd tiles at 0 and 64 (P over the first half of each), O at 128.
-  // Shared memory bounds the blocks per SM to 512 / kCols: one more would wait for tensor memory
+  // Tensor memory: S of even and odd tiles at 0 and 64 (over each, P; its low parts 32 columns on),
+  // O at 128.  Shared memory bounds the blocks per SM to 512 / kCols: one more would wait for tensor memory
   // while its cluster's other blocks hold theirs.
   static constexpr uint32_t kCols = 256;
-  static_assert(kData > 76 * 1024, "two blocks per SM");
+  static_assert(kData > 76 * 1024, "at most two blocks per SM");
 };
 
 struct Params {
-  const uint16_t* q;
+  const void* q;  // 16-bit values, or fp32 (WIDE), as o
   const uint16_t* v;
-  uint16_t* o;
+  void* o;
   const int32_t *parents, *n_nodes, *lens;
   int64_t q_seq, q_node, q_head, o_seq, o_node, o_head, v_seq, v_head, v_row;
   int n, hq, hkv, G, max_seq;
@@ -237,7 +241,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// Whether a 16-bit value is infinite or NaN; its value.
+// Whether a 16-bit value is infinite or NaN; its value; two values as their 16-bit roundings and
+// the roundings of what those left over.
 template <bool FP16>
 __device__ __forceinline__ bool nonfinite16(uint32_t h) {
   constexpr uint32_t e = FP16 ? 0x7c00u : 0x7f80u;
@@ -247,6 +252,12 @@ template <bool FP16>
 __device__ __forceinline__ float value16(uint16_t h) {
   if constexpr (FP16) return __half2float(__ushort_as_half(h));
   return __uint_as_float((uint32_t)h << 16);
+}
+
+template <bool FP16>
+__device__ __forceinline__ void split16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack16<FP16>(x, y);
+  lo = pack16<FP16>(x - value16<FP16>((uint16_t)hi), y - value16<FP16>((uint16_t)(hi >> 16)));
 }
 
 // Address of a peer block's shared memory, and stores there.
@@ -332,27 +343,34 @@ __device__ __forceinline__ bool alive(const Ctl& S, int node) {
   return S.anc[node * kAncStride + (node >> 5)] >> (node & 31) & 1;
 }
 
+template <bool WIDE>
+using Out = typename std::conditional<WIDE, float, uint16_t>::type;
+
 // Infinite and NaN values of drafts that the node sees, added to n output values at `out`.
-template <bool FP16>
+template <bool FP16, bool WIDE>
 __device__ __noinline__ void add_nonfinite(const Params& P, const Ctl& S, int b, int h, int len, int node, int col,
-                                           int n, uint16_t* out) {
+                                           int n, Out<WIDE>* out) {
   if (!alive(S, node)) return;
   for (int a = 0; a <= node; ++a) {
     if (!(S.anc[node * kAncStride + (a >> 5)] >> (a & 31) & 1)) continue;
     const uint16_t* val = P.v + (int64_t)b * P.v_seq + (int64_t)h * P.v_head + (int64_t)(len + a) * P.v_row + col;
-    for (int x = 0; x < n; ++x)
-      if (nonfinite16<FP16>(val[x]))
+    for (int x = 0; x < n; ++x) {
+      if (!nonfinite16<FP16>(val[x])) continue;
+      if constexpr (WIDE)
+        out[x] += value16<FP16>(val[x]);
+      else
         out[x] = (uint16_t)pack16<FP16>(value16<FP16>(out[x]) + value16<FP16>(val[x]), 0.f);
+    }
   }
 }
 
 // Output rows that this block finishes: row r's partial results, weighted, from the C blocks (they
 // lie in this block's shared memory: part p of its x-th row at row p * per + x).  The loops are kept
 // rolled: this runs once, and its instructions come from memory.
-template <int D, bool FP16>
+template <int D, bool FP16, bool WIDE>
 __device__ __forceinline__ void merge(const Params& P, const Ctl& S, const float* parts, int b, int h, int first,
                                       int rows, int per, int rank, int C, int len, int warp, int lane) {
-  using Ge = Geo<D>;
+  using Ge = Geo<D, WIDE>;
   constexpr int kLanes = D / 4, kPer = 32 / kLanes;  // lanes per row, rows per warp side by side
   const int sub = lane / kLanes, in = lane % kLanes, col = in * 4;
   const int r0 = rank * per, r1 = min(rows, r0 + per);
@@ -383,21 +401,25 @@ __device__ __forceinline__ void merge(const Params& P, const Ctl& S, const float
       }
     }
     if (base + sub >= r1) continue;
-    uint16_t* out = P.o + (int64_t)b * P.o_seq + (int64_t)node * P.o_node + (int64_t)(h * P.G + g) * P.o_head + col;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack16<FP16>(acc[0], acc[1]), pack16<FP16>(acc[2], acc[3]));
-    if (S.bad_any) add_nonfinite<FP16>(P, S, b, h, len, node, col, 4, out);
+    Out<WIDE>* out = static_cast<Out<WIDE>*>(P.o) + (int64_t)b * P.o_seq + (int64_t)node * P.o_node +
+                     (int64_t)(h * P.G + g) * P.o_head + col;
+    if constexpr (WIDE)
+      *reinterpret_cast<float4*>(out) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    else
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack16<FP16>(acc[0], acc[1]), pack16<FP16>(acc[2], acc[3]));
+    if (S.bad_any) add_nonfinite<FP16, WIDE>(P, S, b, h, len, node, col, 4, out);
   }
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attention(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ Params P) {
-  using Ge = Geo<D>;
+  using Ge = Geo<D, WIDE>;
   extern __shared__ uint8_t raw[];
   __shared__ Ctl S;
   uint8_t* data = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t* ring = data + Ge::kQTile;
+  uint8_t* ring = data + Ge::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
 
@@ -440,15 +462,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     // Q rows into the swizzled tile: 16-byte piece c of row r goes to piece c ^ (r % 8).  Rows of
     // the tile without a node keep what is there: they only reach their own, unused, results.
     const int c = row % (D / 8), used = min(P.nt, P.n - first) * P.G;
-    const uint16_t* src = P.q + (int64_t)b * P.q_seq + (int64_t)first * P.q_node +
-                          (int64_t)h * P.G * P.q_head + c * 8;
-    const uint32_t dst = smem_u32(data) + (c / 8) * kRows * 128;
+    const int64_t src = (int64_t)b * P.q_seq + (int64_t)first * P.q_node + (int64_t)h * P.G * P.q_head + c * 8;
+    uint8_t* const dst = data + (c / 8) * kRows * 128;
 #pragma unroll 1
     for (int r = row / (D / 8); r < used; r += kRows / (D / 8)) {
       const int lr = (int)(r * P.inv_g >> 16);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + r * 128 + ((c & 7) ^ (r & 7)) * 16),
-                   "l"(src + (int64_t)lr * P.q_node + (int64_t)(r - lr * P.G) * P.q_head)
-                   : "memory");
+      const int64_t at = src + (int64_t)lr * P.q_node + (int64_t)(r - lr * P.G) * P.q_head;
+      uint8_t* to = dst + r * 128 + ((c & 7) ^ (r & 7)) * 16;
+      if constexpr (WIDE) {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(P.q) + at);
+        const float4 x = f[0], y = f[1];
+        uint4 hi, lo;
+        split16<FP16>(x.x, x.y, hi.x, lo.x);
+        split16<FP16>(x.z, x.w, hi.y, lo.y);
+        split16<FP16>(y.x, y.y, hi.z, lo.z);
+        split16<FP16>(y.z, y.w, hi.w, lo.w);
+        *reinterpret_cast<uint4*>(to) = hi;
+        *reinterpret_cast<uint4*>(to + Ge::kQTile) = lo;
+      } else {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                     "l"(static_cast<const uint16_t*>(P.q) + at)
+                     : "memory");
+      }
     }
   }
   __syncwarp();
@@ -520,6 +555,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int s = 0; s < kKeys / 16; ++s)
               mma_ts(tm + 128, tm + buf * 64 + s * 8, vd + s * (2048 >> 4), idesc_o, j != 0 || s != 0);
+            if constexpr (WIDE)
+#pragma unroll
+              for (int s = 0; s < kKeys / 16; ++s)
+                mma_ts(tm + 128, tm + buf * 64 + 32 + s * 8, vd + s * (2048 >> 4), idesc_o, 1);
             tc_commit(&S.o_done);
             tc_commit(&S.empty[stage]);
           }
@@ -536,6 +575,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int s = 0; s < D / 16; ++s)
               tc_mma_f16(tm + buf * 64, q_desc + (((s / 4) * kRows * 128 + (s % 4) * 32) >> 4),
                          kd + (((s / 4) * kKeys * 128 + (s % 4) * 32) >> 4), idesc_s, s != 0);
+            if constexpr (WIDE)
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s)
+                tc_mma_f16(tm + buf * 64, q_desc + ((Ge::kQTile + (s / 4) * kRows * 128 + (s % 4) * 32) >> 4),
+                           kd + (((s / 4) * kKeys * 128 + (s % 4) * 32) >> 4), idesc_s, 1);
             tc_commit(&S.s_full[buf]);
             tc_commit(&S.empty[stage]);
           }
@@ -669,14 +713,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           e[x] = pack2(ex2(y.x), ex2(y.y));
         }
         uint64_t sum[4] = {e[0], e[1], e[2], e[3]};
-        uint32_t p[kKeys / 2];
+        uint32_t p[kKeys / 2], low[WIDE ? kKeys / 2 : 1];
 #pragma unroll
         for (int x = 0; x < kKeys / 2; ++x) {
           const float2 y = unpack2(e[x]);
-          p[x] = pack16<FP16>(y.x, y.y);
+          if constexpr (WIDE)
+            split16<FP16>(y.x, y.y, p[x], low[x]);
+          else
+            p[x] = pack16<FP16>(y.x, y.y);
           if (x >= 4) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[x & 3]) : "l"(e[x]));
         }
         tmem_st32(s_at + (j & 1) * 64, p);  // over scores that are read
+        if constexpr (WIDE) tmem_st32(s_at + (j & 1) * 64 + 32, low);
         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[0]) : "l"(sum[1]));
         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[2]) : "l"(sum[3]));
         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[0]) : "l"(sum[2]));
@@ -698,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (C == 1) {
         if (ok) ok = wait_warp(&S.anc_full, 0, P, S);
         const float inv = l == 0.f || !real || !alive(S, node) ? 0.f : 1.f / l;
-        uint16_t* out = P.o + (int64_t)b * P.o_seq + (int64_t)node * P.o_node +
-                        (int64_t)(h * P.G + row - local * P.G) * P.o_head;
+        Out<WIDE>* out = static_cast<Out<WIDE>*>(P.o) + (int64_t)b * P.o_seq + (int64_t)node * P.o_node +
+                         (int64_t)(h * P.G + row - local * P.G) * P.o_head;
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           uint32_t o[32];
@@ -709,16 +757,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (real)
 #pragma unroll
             for (int x = 0; x < 32; x += 8) {
-              uint32_t p[4];
+              float f[8];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float f0 = __uint_as_float(o[x + 2 * y]), f1 = __uint_as_float(o[x + 2 * y + 1]);
-                p[y] = inv == 0.f ? 0u : pack16<FP16>(f0 * inv, f1 * inv);
+              for (int y = 0; y < 8; ++y) f[y] = inv == 0.f ? 0.f : __uint_as_float(o[x + y]) * inv;
+              if constexpr (WIDE) {
+                *reinterpret_cast<float4*>(out + k * 32 + x) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4*>(out + k * 32 + x + 4) = make_float4(f[4], f[5], f[6], f[7]);
+              } else {
+                *reinterpret_cast<uint4*>(out + k * 32 + x) = make_uint4(
+                    pack16<FP16>(f[0], f[1]), pack16<FP16>(f[2], f[3]), pack16<FP16>(f[4], f[5]), pack16<FP16>(f[6], f[7]));
               }
-              *reinterpret_cast<uint4*>(out + k * 32 + x) = make_uint4(p[0], p[1], p[2], p[3]);
             }
         }
-        if (S.bad_v && real) add_nonfinite<FP16>(P, S, b, h, len, node, 0, D, out);
+        if (S.bad_v && real) add_nonfinite<FP16, WIDE>(P, S, b, h, len, node, 0, D, out);
       } else {
         // a row's statistics and O to the block that finishes it, over that block's Q and ring
         const int owner = real ? row / per : 0, x = row - owner * per;
@@ -770,13 +821,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   if (warp == kMmaWarp) tc_dealloc(tmem, Ge::kCols);
   if (C > 1 && on)
-    merge<D, FP16>(P, S, reinterpret_cast<const float*>(data), b, h, first, rows, per, rank, C, len, warp, lane);
+    merge<D, FP16, WIDE>(P, S, reinterpret_cast<const float*>(data), b, h, first, rows, per, rank, C, len, warp, lane);
 }
 
 // Clusters of 2, 4, 8 and 16 blocks that the device runs at once, asked once per device and kernel.
-// (The query counts one block per SM for this kernel at any size of shared memory; two run, by
-// their active warps, so its answer is doubled.)
-template <int D, bool FP16>
+// (The query counts one block per SM for this kernel at any size of shared memory; two run where
+// that has room for them, by their active warps, and its answer is doubled there.)
+template <int D, bool FP16, bool WIDE>
 static cudaError_t clusters_at_once(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int* fit) {
   static std::atomic<uint64_t> known[64];  // four counts of 16 bits, 1 + each
   int dev = 0;
@@ -784,7 +835,7 @@ static cudaError_t clusters_at_once(cudaLaunchConfig_t& cfg, cudaLaunchAttribute
   if (e != cudaSuccess) return e;
   uint64_t v = dev < 64 ? known[dev].load() : 0;
   if (!v) {
-    const auto kernel = tree_attention<D, FP16>;
+    const auto kernel = tree_attention<D, FP16, WIDE>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)  // two blocks per SM need nearly all of its shared memory
@@ -802,23 +853,24 @@ static cudaError_t clusters_at_once(cudaLaunchConfig_t& cfg, cudaLaunchAttribute
     }
     if (dev < 64) known[dev].store(v);
   }
-  for (int k = 0; k < 4; ++k) fit[k] = 2 * ((int)(v >> (16 * k) & 0xffff) - 1);
+  const int per_sm = cfg.dynamicSmemBytes > 100 * 1024 ? 1 : 2;
+  for (int k = 0; k < 4; ++k) fit[k] = per_sm * ((int)(v >> (16 * k) & 0xffff) - 1);
   return cudaSuccess;
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, bool WIDE>
 static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params& P, int B, int n_sms, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Geo<D>::kData + 1024;
+  cfg.dynamicSmemBytes = Geo<D, WIDE>::kData + 1024;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int fit[4];
-  const cudaError_t e = clusters_at_once<D, FP16>(cfg, attr, fit);
+  const cudaError_t e = clusters_at_once<D, FP16, WIDE>(cfg, attr, fit);
   if (e != cudaSuccess) return e;
   P.units = (P.n + P.nt - 1) / P.nt;
   const int64_t units = (int64_t)B * P.hkv * P.units;
@@ -832,7 +884,7 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params&
   int C = 1;
   double best = 0.0;
   for (int k = 0; k < 5 && (k == 0 || (int64_t)kKeys << (k - 1) < P.max_seq); ++k) {
-    const int at_once = k == 0 ? 2 * n_sms : fit[k - 1];
+    const int at_once = k == 0 ? (cfg.dynamicSmemBytes > 100 * 1024 ? 1 : 2) * n_sms : fit[k - 1];
     if (at_once < 1) continue;
     const double turns = (double)units / at_once;
     const double t = (8.0 + tiles / (1 << k)) * (units << k > n_sms ? 1.5 : 1.0) *
@@ -841,7 +893,7 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params&
   }
   attr[0].val.clusterDim.x = C;
   cfg.gridDim = dim3((unsigned)(units * C));
-  return cudaLaunchKernelEx(&cfg, tree_attention<D, FP16>, mk_, mv, P);
+  return cudaLaunchKernelEx(&cfg, tree_attention<D, FP16, WIDE>, mk_, mv, P);
 }
 
 static bool encode(CUtensorMap* map, const void* base, int fp16, int D, int max_seq, int hkv, int B, int64_t seq,
@@ -863,9 +915,9 @@ int tree_attention(const mk_tree_shape& s, const void* q, const void* k, const v
                    cudaStream_t stream, std::string* err) {
   using namespace tree;
   Params P;
-  P.q = static_cast<const uint16_t*>(q);
+  P.q = q;
   P.v = static_cast<const uint16_t*>(v);
-  P.o = static_cast<uint16_t*>(o);
+  P.o = o;
   P.parents = parents, P.n_nodes = n_nodes, P.lens = lens;
   P.q_seq = s.q_seq, P.q_node = s.q_node, P.q_head = s.q_head;
   P.o_seq = s.o_seq, P.o_node = s.o_node, P.o_head = s.o_head;
@@ -885,10 +937,12 @@ int tree_attention(const mk_tree_shape& s, const void* q, const void* k, const v
     return MK_ERR_INVALID_ARG;
   }
   cudaError_t e;
+#define MK_LAUNCH(D, F) (s.wide ? launch<D, F, true>(mk_, mv, P, s.B, n_sms, stream) : launch<D, F, false>(mk_, mv, P, s.B, n_sms, stream))
   if (s.head_dim == 128)
-    e = fp16 ? launch<128, true>(mk_, mv, P, s.B, n_sms, stream) : launch<128, false>(mk_, mv, P, s.B, n_sms, stream);
+    e = fp16 ? MK_LAUNCH(128, true) : MK_LAUNCH(128, false);
   else
-    e = fp16 ? launch<64, true>(mk_, mv, P, s.B, n_sms, stream) : launch<64, false>(mk_, mv, P, s.B, n_sms, stream);
+    e = fp16 ? MK_LAUNCH(64, true) : MK_LAUNCH(64, false);
+#undef MK_LAUNCH
   if (e != cudaSuccess) {
     *err = std::string("tree_attention launch: ") + cudaGetErrorString(e);
     return MK_ERR_CUDA;

@@ -21,6 +21,16 @@ def ancestors(parents, n_nodes):
     return out
 
 
+def wide_bound(o, a, v, dtype):
+    """The same for fp32 q and o over a 16-bit cache.  q and P enter as two parts, each off by at most
+    h^2, h = eps / 2: h^2 A from P, and from q, with |q|.|k| scale below 16, weights off by 16 h^2.  S
+    sums up to 256 products in fp32: 256 x 2^-24 x 16 = 2^-12; exp2, the sums and the merge 2^-13.  The
+    weights' sum moves as well: twice that.  fp16 parts below 2^-14 are multiples of 2^-24 (x 2^-7)."""
+    h2 = (torch.finfo(dtype).eps / 2) ** 2
+    tiny = 2.0 ** -31 * v.double().abs().amax() * v.shape[2] if dtype == torch.float16 else 1e-30
+    return 2.0 ** -24 * o.abs() + (h2 + 2 * (16 * h2 + 2.0 ** -12 + 2.0 ** -13)) * a + tiny
+
+
 def random_tree(rng, n, kind):
     if kind == "chain":
         return np.arange(n, dtype=np.int32) - 1

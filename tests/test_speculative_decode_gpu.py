@@ -1,0 +1,154 @@
+"""The speculative operators together, as a decoding loop uses them: tree forward, verification,
+commit, reorder, and ordinary decode steps on the cache that they leave."""
+import numpy as np
+import pytest
+import torch
+
+import mk_inputs as mi
+import oracle
+import persistent_megakernel_decode_04_b200 as mk
+from _parity import ARGMAX_MARGIN, argmax_agrees, kv_close, logits_close
+from _speculative import ancestors
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def model(shape, max_batch, max_seq, seed=5, tc_min=0):
+    w = mi.make_weights(shape, seed=seed)
+    cfg = mk.Config.from_shape(w.shape, max_batch, max_seq)
+    cfg.tc_min_batch = tc_min
+    return w, mk.Megakernel(cfg, w, 0)
+
+
+@pytest.mark.parametrize("shape,max_batch,B,tc_min", [(mi.TINY, 1, 1, 0), (mi.TINY, 4, 3, 0), (mi.TINY, 4, 3, 5),
+                                                      (mi.TINY, 16, 2, 0), (mi.TINY_QK, 1, 1, 0), (mi.TINY_QK, 16, 2, 0)])
+def test_tree_forward_matches_the_oracle_on_every_path(shape, max_batch, B, tc_min):
+    w, m = model(shape, max_batch, 64, tc_min=tc_min)
+    rng = np.random.default_rng(B)
+    T = [9 + 3 * b for b in range(B)]
+    n = 7
+    parents = np.array([-1, 0, 0, 1, 1, 2, 3], dtype=np.int32)
+    tokens = rng.integers(0, w.shape.vocab, (B, n)).astype(np.int32)
+    prompts = [mi.prompt(5, b, T[b], w.shape.vocab) for b in range(B)]
+    # the prompts, one after another, as trees that are chains; each is committed whole
+    lens = i32([0] * B)
+    t_max = max(T)
+    toks = np.zeros((B, t_max), dtype=np.int32)
+    for b in range(B):
+        toks[b, :T[b]] = prompts[b]
+    chain = i32(np.tile(np.arange(t_max) - 1, (B, 1)))
+    first = m.tree_forward(i32(toks), chain, lens, i32(T))
+    lens = m.commit(i32(np.tile(np.arange(t_max), (B, 1))), i32(T), lens)
+    assert lens.tolist() == T
+    logits = m.tree_forward(i32(tokens), i32(np.tile(parents, (B, 1))), lens).cpu().numpy()
+    assert mk.mk_tree_attention_status() == mk.MK_OK
+    paths = ancestors(parents, n)
+    for b in range(B):
+        for i in range(n):
+            ref = oracle.Decoder(w, 1, 64)
+            rl = ref.prefill(np.concatenate([prompts[b], tokens[b, paths[i]]])[None])[0]
+            logits_close(logits[b, i], rl, f"seq {b} node {i}")
+        ref = oracle.Decoder(w, 1, 64)
+        rl = ref.prefill(prompts[b][None])[0]
+        logits_close(first[b, T[b] - 1].cpu().numpy(), rl, f"prompt {b}")
+        kv_close(m.kv_view()[:, :, b:b + 1, :, :T[b], :].cpu().numpy(), ref.get_cache(T[b]), f"cache {b}")
+    m.close()
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+def test_greedy_speculation_emits_the_greedy_text(sampled):
+    """Drafts that are sometimes right: whatever they are, the tokens are the target's own choices;
+    then plain decode steps go on from the committed cache."""
+    w, m = model(mi.TINY, 4, 128)
+    B, V, T, n = 3, w.shape.vocab, 8, 9
+    rng = np.random.default_rng(1)
+    prompts = np.stack([mi.prompt(7, b, T, V) for b in range(B)])
+    m.prefill(i32(prompts[:, :T - 1]))  # the last prompt token is the first tree's root
+    lens = i32([T - 1] * B)
+    text = [list(prompts[b]) for b in range(B)]
+    ws = torch.empty(mk.mk_tree_verify_workspace_bytes(B, n, V), dtype=torch.uint8, device=DEV)
+    oracles = [oracle.Decoder(w, 1, 128) for _ in range(B)]
+    rl = [oracles[b].prefill(prompts[b][None])[0] for b in range(B)]
+    accepted = 0
+    for step in range(6):
+        parents = np.tile(np.array([-1, 0, 0, 1, 1, 2, 3, 3, 6], dtype=np.int32), (B, 1))
+        tokens = rng.integers(0, V, (B, n)).astype(np.int32)
+        for b in range(B):
+            tokens[b, 0] = text[b][-1]
+            if step % 3 != 2:  # the true continuation along 0-1-3, or 0-2-5
+                ref = oracle.Decoder(w, 1, 128)
+                t = oracle.argmax(ref.prefill(np.array(text[b], dtype=np.int32)[None])[0])
+                for node in ((1, 3, 6) if step % 3 == 0 else (2, 5)):
+                    tokens[b, node] = t
+                    t = oracle.argmax(ref.decode(np.array([t], dtype=np.int32))[0])
+        logits = m.tree_forward(i32(tokens), i32(parents), lens)
+        path, n_path, nxt = i32(np.zeros((B, n))), i32([0] * B), i32([0] * B)
+        mk.mk_tree_verify(logits, torch.randn_like(logits) if sampled else None, i32(tokens), i32(parents), None,
+                          torch.rand(B, n, device=DEV), torch.rand(B, device=DEV), torch.zeros(B, device=DEV),
+                          torch.ones(B, device=DEV) if sampled else None, path, n_path, nxt, ws)
+        new_lens = m.commit(path, n_path, lens)
+        assert (new_lens == lens + n_path).all()
+        for b in range(B):
+            kept = path[b, 1:int(n_path[b])].tolist()
+            accepted += len(kept)
+            for t in [int(tokens[b, i]) for i in kept] + [int(nxt[b])]:
+                margin = np.sort(rl[b].astype(np.float64))[-2:]
+                assert t == oracle.argmax(rl[b]) or margin[1] - margin[0] <= ARGMAX_MARGIN
+                text[b].append(t)
+                rl[b] = oracles[b].decode(np.array([t], dtype=np.int32))[0]
+            assert int(new_lens[b]) == len(text[b]) - 1
+        lens = new_lens
+    assert accepted >= 2 * B
+    m.set_positions(lens.tolist())
+    for b in range(B):
+        kv_close(m.kv_view()[:, :, b:b + 1, :, :int(lens[b]), :].cpu().numpy(), oracles[b].get_cache(int(lens[b])), f"seq {b}")
+    got, nt = m.decode(i32([text[b][-1] for b in range(B)]))
+    for b in range(B):
+        logits_close(got[b].cpu().numpy(), rl[b], f"decode after speculation, seq {b}")
+        assert argmax_agrees(got[b].cpu().numpy(), rl[b], int(nt[b]))
+    assert m.sync_status() == mk.MK_OK
+    m.close()
+
+
+def test_forked_prompt_decodes_like_its_source():
+    w, m = model(mi.TINY, 4, 64)
+    T = 11
+    prompt = mi.prompt(3, 0, T, w.shape.vocab)
+    m.prefill(i32(prompt[None]))
+    lens = m.reorder(i32([0, 0, 0, 0]), i32([T, 0, 5, 9]))
+    assert lens.tolist() == [T] * 4
+    m.set_positions(lens.tolist())
+    toks = [3, 500, 77, 3]
+    got, _ = m.decode(i32(toks))
+    for b in range(4):
+        ref = oracle.Decoder(w, 1, 64)
+        ref.prefill(prompt[None])
+        logits_close(got[b].cpu().numpy(), ref.decode(np.array([toks[b]], dtype=np.int32))[0], f"fork {b}")
+    assert torch.equal(got[0], got[3])
+    m.close()
+
+
+def test_tree_forward_at_the_caches_end():
+    w, m = model(mi.TINY, 2, 32)
+    prompts = np.stack([mi.prompt(4, b, 30, w.shape.vocab) for b in range(2)])
+    m.prefill(i32(prompts))
+    before = m.kv_view().clone()
+    toks = i32([[1, 2, 3, 4, 5]] * 2)
+    logits = m.tree_forward(toks, i32([[-1, 0, 1, 2, 3]] * 2), i32([30, 12]))
+    for b, ln in ((0, 30), (1, 12)):
+        ref = oracle.Decoder(w, 1, 32)
+        ref.prefill(prompts[b][None, :ln])
+        for i in range(min(5, 32 - ln)):
+            logits_close(logits[b, i].cpu().numpy(), ref.decode(np.array([i + 1], dtype=np.int32))[0], f"{b} {i}")
+    after = m.kv_view()
+    assert torch.equal(after[:, :, 0, :, :30], before[:, :, 0, :, :30])
+    assert torch.equal(after[:, :, 1, :, :12], before[:, :, 1, :, :12])
+    assert torch.equal(after[:, :, 1, :, 17:], before[:, :, 1, :, 17:])
+    with pytest.raises(mk.MkError):
+        m.tree_forward(i32([[0] * 40] * 2), i32([[-1] * 40] * 2), i32([0, 0]))  # 80 rows: scratch for 64
+    m.close()

@@ -10,7 +10,7 @@ OK = 1 << 20  # a 16-byte aligned address that is never used
 
 
 def tree_shape(**kw):
-    f = dict(dtype=mk.MK_BF16, B=2, n=8, n_q_heads=8, n_kv_heads=2, head_dim=64, max_seq=128, q_seq=8 * 8 * 64,
+    f = dict(dtype=mk.MK_BF16, wide=0, B=2, n=8, n_q_heads=8, n_kv_heads=2, head_dim=64, max_seq=128, q_seq=8 * 8 * 64,
              q_node=8 * 64, q_head=64, k_seq=2 * 128 * 64, k_head=128 * 64, k_row=64, v_seq=2 * 128 * 64,
              v_head=128 * 64, v_row=64, o_seq=8 * 8 * 64, o_node=8 * 64, o_head=64)
     f.update(kw)
@@ -21,7 +21,7 @@ def attend(shape, q=OK, k=OK, v=OK, o=OK, parents=OK, n_nodes=None, lens=OK, sca
     return mk._lib.mk_tree_attention(ctypes.byref(shape) if shape else None, q, k, v, o, parents, n_nodes, lens, scale, None)
 
 
-@pytest.mark.parametrize("kw", [dict(dtype=mk.MK_FP32), dict(dtype=-1), dict(B=0), dict(n=0), dict(n=257), dict(max_seq=0),
+@pytest.mark.parametrize("kw", [dict(dtype=mk.MK_FP32), dict(dtype=-1), dict(wide=2), dict(B=0), dict(n=0), dict(n=257), dict(max_seq=0),
                                 dict(head_dim=96), dict(n_kv_heads=3), dict(n_kv_heads=0), dict(n_q_heads=0),
                                 dict(n_q_heads=258, n_kv_heads=2), dict(q_node=4), dict(k_row=0), dict(k_row=-64),
                                 dict(v_head=100), dict(o_seq=1), dict(k_seq=1 << 40)])
@@ -105,6 +105,8 @@ def test_binding_refuses_tensors_that_do_not_fit():
     refused(mk.mk_tree_attention, q, k, k[:, :1], q.clone(), par, None, ln, 0.1)
     refused(mk.mk_tree_attention, q.transpose(2, 3), k, k, q.transpose(2, 3), par, None, ln, 0.1)
     refused(mk.mk_tree_attention, q.double(), k, k, q.clone(), par, None, ln, 0.1)
+    refused(mk.mk_tree_attention, q.float(), k, k, q.clone(), par, None, ln, 0.1)
+    refused(mk.mk_tree_attention, q.float(), k.float(), k.float(), q.float(), par, None, ln, 0.1)
     t = torch.zeros(2, 4, 100)
     f, one = torch.zeros(2, 4), torch.zeros(2)
     out = [torch.zeros(2, 4, dtype=torch.int32), ln.clone(), ln.clone()]
@@ -117,3 +119,13 @@ def test_binding_refuses_tensors_that_do_not_fit():
     refused(mk.mk_cache_commit, kv, par, ln, ln, ln.clone())
     refused(mk.mk_cache_commit, kv.transpose(0, 1), par, ln, ln, ln.clone())
     refused(mk.mk_cache_reorder, kv.float(), ln, ln, ln.clone())
+
+
+def test_tree_forward_refusals():
+    import mk_inputs as mi
+    assert mk._lib.mk_tree_forward(None, OK, OK, None, OK, 1, 4, OK, OK, None) == mk.MK_ERR_INVALID_ARG
+    ctx = mk.mk_build_taskgraph(mk.Config.from_shape(mi.TINY, 2, 64).c(), -1)
+    try:
+        assert mk._lib.mk_tree_forward(ctx, OK, OK, None, OK, 1, 4, OK, OK, None) == mk.MK_ERR_STATE
+    finally:
+        mk.mk_destroy(ctx)

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import persistent_megakernel_decode_04_b200 as mk
-from _speculative import attention_bound, attention_rows, random_tree
+from _speculative import attention_bound, attention_rows, random_tree, wide_bound
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -57,6 +57,30 @@ def check(x, scale, got):
 def test_matches_the_definition(B, n, hq, hkv, d, S, lens, dtype):
     x = make(B, n, hq, hkv, d, S, lens, dtype=dtype, seed=n)
     check(x, d ** -0.5, run(x, d ** -0.5))
+
+
+@pytest.mark.parametrize("B,n,hq,hkv,d,S,lens", [
+    (1, 1, 4, 2, 64, 64, [0]), (2, 7, 32, 8, 128, 1024, [551, 1017]), (3, 33, 6, 2, 128, 700, [126, 127, 128]),
+    (2, 65, 14, 2, 64, 900, [255, 830]), (12, 13, 16, 16, 128, 300, [20 * b for b in range(12)]),
+])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_fp32_queries_and_outputs_over_a_16_bit_cache(B, n, hq, hkv, d, S, lens, dtype):
+    x = make(B, n, hq, hkv, d, S, lens, dtype=dtype, seed=n)
+    x["q"] = torch.randn(B, n, hq, d, generator=torch.Generator().manual_seed(n + 1))
+    scale = d ** -0.5
+    got = run(x, scale)
+    ref, a = attention_rows(x["q"], x["k"], x["v"], x["parents"], None, x["lens"], scale)
+    err = (got.double() - ref).abs()
+    room = wide_bound(ref, a, x["v"], dtype)
+    assert (err <= room).all(), (err / room).max()
+    narrow = run(dict(x, q=x["q"].to(dtype)), scale).double() - ref  # the same without the low parts
+    assert err.square().mean().sqrt().item() <= narrow.square().mean().sqrt().item() / 8  # (one key: 0 and 0)
+    # NaN in rows that are not seen, and a negative scale, as in the other form
+    y = dict(x, k=x["k"].clone(), v=x["v"].clone())
+    for b in range(B):
+        y["k"][b, :, lens[b] + n:], y["v"][b, :, lens[b] + n:] = float("nan"), float("inf")
+    assert torch.equal(run(y, scale), got)
+    assert torch.equal(run(dict(x, q=-x["q"]), -scale), got)
 
 
 @pytest.mark.parametrize("kind", ["chain", "star", "forest"])

@@ -39,9 +39,11 @@ constexpr int kChunk = 8192;        // elements of a row per block of row_stats
 constexpr int kThreads = 512;       // walk
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kPer = 8;              // elements per thread and step of a pass
-constexpr int kPass = kThreads * kPer;
 constexpr float kClose = 1e-5f;
+// elements per thread and step of a pass: eight keep more exponentials in flight; without a draft
+// four need few enough registers for row_stats's blocks beside the walk's
+template <bool DRAFT>
+constexpr int kPerOf = DRAFT ? 8 : 4;
 constexpr int kMaxDyn = 192 * 1024;  // walk: dynamic shared memory
 
 struct Stat {  // of one row's chunk
@@ -245,8 +247,7 @@ struct Ctl {
   double total;                    // of the last pass
   double iP, iQ, iZ[kMaxNodes];    // 1 / sum of a node's exponentials; 1 / sum of its rests so far
   double p[kMaxNodes], q[kMaxNodes];  // exponentials of a child's token in its parent's rows
-  double inv[kMaxNodes];              // 1 / sum of a node's exponentials by the fp32 statistics
-  float m[2][kMaxNodes], z[2][kMaxNodes], u[kMaxNodes], logit[2][kMaxNodes];
+  float m[2][kMaxNodes], z[2][kMaxNodes], u[kMaxNodes], logit[2][kMaxNodes], pf[kMaxNodes];  // pf: a child's probability
   int idx[kMaxNodes];
   int32_t token[kMaxNodes], gone[kMaxNodes];  // of a child; of the current node's rejected children
   int16_t parent[kMaxNodes];
@@ -256,8 +257,9 @@ struct Ctl {
   int kept;  // rejections that the kept values stand for (0: the exponentials), -1: none are kept
 };
 
-template <typename T>
+template <typename T, bool DRAFT>
 __global__ void __launch_bounds__(kThreads) walk(const Params P) {
+  constexpr int kPer = kPerOf<DRAFT>, kPass = kThreads * kPer;
   __shared__ Ctl S;
   // this block's slice of a row: the last pass's values of it (element k of thread t in step s at
   // (s kPer + k) kThreads + t), the draft's exponentials alike, and sums of 32 kPer elements each
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int b = blockIdx.x / C, n = P.n, V = P.V, nn = in_use(P, b);
   const float temp = P.temperature ? P.temperature[b] : 1.f;
-  const bool greedy = temp == 0.f, sampled = P.draft != nullptr && !greedy;
+  const bool greedy = temp == 0.f, sampled = DRAFT && !greedy;
   const double kLog2e = 1.44269504088896340736;
   const double tc = kLog2e / (double)temp;
   const double dc = sampled ? kLog2e / (double)(P.draft_temperature ? P.draft_temperature[b] : 1.f) : 0.0;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       q = exp2_table(fma((double)ld, dc, -((double)md * dc)), (ld - md) * dcf <= -1000.f, S.table);
     }
     S.p[tid] = p, S.q[tid] = q;
-    S.inv[tid] = 1.0 / (double)S.z[0][tid];
+    if (!DRAFT) S.pf[tid] = par >= 0 && par < tid ? (float)p / S.z[0][par] : 0.f;
     if (par >= 0 && par < tid) {
       // u q / ZQ < p / ZP without divisions
       const double a = (double)S.u[tid] * (sampled ? q : 1.0) * (double)S.z[0][par];
@@ -347,12 +349,14 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   }
   __syncthreads();
 
-  // Thread 0 of every block walks; what it decides follows from the same numbers in each.
+  // Warp 0 of every block walks, its lanes alike; what it decides follows from the same numbers in
+  // each block.
   int32_t* path = P.path + (int64_t)b * n;
-  int cur = 0, depth = nn > 0 ? 1 : 0, c = 1;  // thread 0's
+  int cur = 0, depth = nn > 0 ? 1 : 0, c = 1;  // warp 0's
   bool exact = false;                          // iP, iQ are the current node's
   bool summed = false;                         // `piece` holds the current P
-  double left = 1.0;                           // without draft: what of P is not gone
+  float left = 1.f;                            // without draft: what of P is not gone,
+  double left_exact = 1.0;                     // and the same from exact sums
   if (tid == 0) S.rounds = S.n_gone = 0, S.kept = -1;
   int turn = 0;
   const int slice = (((V + 3 + (int)C - 1) / (int)C) + 3) & ~3;  // elements per block
@@ -360,61 +364,76 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   double* const kept_v = dyn + tid;
   double* const kept_q = kept_v + room;
   double* const piece = dyn + P.keep * room;
+  __syncwarp();
   for (;;) {
-    if (tid == 0) {
+    if (warp == 0) {
       int op = OP_DONE;
       int rounds = S.rounds, n_gone = S.n_gone;
-      for (; c < nn; ++c) {
-        if (S.parent[c] != cur) continue;
+      for (;;) {
+        // the current node's next child from c on
+        uint32_t kids = 0;
+        int base = c;
+        for (; base < nn; base += 32) {
+          kids = __ballot_sync(0xffffffffu, base + lane < nn && S.parent[base + lane] == cur);
+          if (kids) break;
+        }
+        c = kids ? base + __ffs(kids) - 1 : nn;
+        if (c >= nn) break;
         bool take;
         if (greedy) {
           const int x = S.token[c];
-          if (x < 0 || x != S.idx[cur]) continue;
-          take = true;
-        } else if (!exact && n_gone == 0) {
-          if (S.first[c] == 2) {
+          take = x >= 0 && x == S.idx[cur];
+        } else if (!exact) {
+          int first = S.first[c];
+          if (!DRAFT && n_gone > 0) {
+            // (fp32 statistics and this sum know what is left to kClose + 6e-8 per term)
+            const float p = S.again[c] ? 0.f : S.pf[c], a = S.u[c] * left, top = fmaxf(a, p);
+            first = left < 0.125f || (fabsf(a - p) * left <= (kClose + 6e-8f * n_gone) * top && top > 0.f) ? 2 : a < p;
+          }
+          if (first == 2) {
             op = OP_SUMS;  // too close for fp32 statistics: come back with exact ones
             break;
           }
-          take = S.first[c];
+          take = first;
         } else {
-          const double iP = exact ? S.iP : S.inv[cur];
-          double p = S.p[c] * iP, a = (double)S.u[c];
+          double p = S.p[c] * S.iP, a = (double)S.u[c];
           if (sampled) {
             const double q = S.q[c] * S.iQ;
             for (int k = 0; k < rounds; ++k) p = fmax(p - q, 0.0) * S.iZ[k];
             a *= q;
           } else {
             if (S.again[c]) p = 0.0;
-            a *= left;
-            // (fp32 statistics know what is left to kClose)
-            if (!exact && (left < 0.125 || fabs(a - p) * left <= (double)kClose * fmax(a, p))) {
-              op = OP_SUMS;
-              break;
-            }
+            a *= left_exact;
           }
           take = a < p;
         }
         if (take) {
-          if (rank == 0) path[depth] = c;
+          if (rank == 0 && lane == 0) path[depth] = c;
           ++depth;
           cur = c;
           exact = summed = false;
           rounds = n_gone = 0;
-          left = 1.0;
+          left = 1.f;
+        } else if (greedy) {
         } else if (sampled) {
           op = exact ? OP_REST : OP_SUMS;  // rejected: what is left of P
           break;
         } else if (!S.again[c]) {
-          S.gone[n_gone++] = c;
-          left -= S.p[c] * (exact ? S.iP : S.inv[cur]);
+          if (lane == 0) S.gone[n_gone] = c;
+          ++n_gone;
+          left -= S.pf[c];
+          if (exact) left_exact -= S.p[c] * S.iP;
           summed = false;
         }
+        ++c;
       }
       if (op == OP_DONE && !greedy && nn > 0 && !summed) op = rounds > 0 ? OP_AGAIN : OP_SUMS;
-      S.rounds = rounds, S.n_gone = n_gone;
-      S.op = op;
-      S.cur = cur;
+      __syncwarp();
+      if (lane == 0) {
+        S.rounds = rounds, S.n_gone = n_gone;
+        S.op = op;
+        S.cur = cur;
+      }
     }
     __syncthreads();
     const int op = S.op;
@@ -456,10 +475,10 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     const bool q_from_kept = from_kept && P.keep > 1;
     const double scale = rounds > 1 ? S.iZ[rounds > 1 ? rounds - 2 : 0] : iP;
     double sv = 0.0, sq = 0.0;
+    float tl[kPer], dl[kPer] = {};
 #pragma unroll 1
     for (int s = 0, j = lo + tid * kPer; lo + s * kPass < hi; ++s, j += kPass) {
       double v[kPer], q[kPer];
-      float tl[kPer], dl[kPer];
       double* const at_v = kept_v + s * kPass;
       double* const at_q = kept_q + s * kPass;
       if (!from_kept)
@@ -514,7 +533,8 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
             if (at == k) v[k] = 0.0;
         }
       }
-      double w = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      double w = (v[0] + v[1]) + (v[2] + v[3]);
+      if constexpr (kPer == 8) w += (v[4] + v[5]) + (v[6] + v[7]);
 #pragma unroll
       for (int off = 16; off; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
       if (lane == 0) piece[s * kWarps + warp] = w;
@@ -539,27 +559,32 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         t += __shfl_xor_sync(0xffffffffu, t, off);
         z += __shfl_xor_sync(0xffffffffu, z, off);
       }
-      if (lane == 0) {
-        S.total = t;
-        if (op == OP_SUMS) {
-          // what was taken out of P belongs to the sum of its exponentials
-          for (int k = 0; k < S.n_gone; ++k) t += S.p[S.gone[k]];
-          S.iP = 1.0 / t, S.iQ = 1.0 / z;
-          exact = summed = true;
-          left = 1.0;
-          for (int k = 0; k < S.n_gone; ++k) left -= S.p[S.gone[k]] * S.iP;
-          S.kept = 0;
-        } else if (op == OP_AGAIN) {
-          summed = true;
-          S.kept = S.rounds;
-        } else {
-          // (a sum that is NaN counts as something: the draw then finds no distribution)
-          summed = !(t <= 0.0);
-          if (summed) S.iZ[S.rounds++] = 1.0 / t;  // else nothing would be left: P stays
-          S.kept = summed ? S.rounds : -1;
-          ++c;  // this child is dealt with
+      if (lane == 0) S.total = t;
+      if (op == OP_SUMS) {
+        // what was taken out of P belongs to the sum of its exponentials
+        for (int k = 0; k < S.n_gone; ++k) t += S.p[S.gone[k]];
+        const double iP = 1.0 / (lane == 1 ? z : t);
+        if (lane == 0) S.iP = iP, S.kept = 0;
+        if (lane == 1) S.iQ = iP;
+        exact = summed = true;
+        if (!DRAFT) {
+          __syncwarp();
+          left_exact = 1.0;
+          for (int k = 0; k < S.n_gone; ++k) left_exact -= S.p[S.gone[k]] * S.iP;
         }
+      } else if (op == OP_AGAIN) {
+        summed = true;
+        if (lane == 0) S.kept = S.rounds;
+      } else {
+        // (a sum that is NaN counts as something: the draw then finds no distribution)
+        summed = !(t <= 0.0);  // else nothing would be left: P stays
+        if (lane == 0) {
+          if (summed) S.iZ[S.rounds++] = 1.0 / t;
+          S.kept = summed ? S.rounds : -1;
+        }
+        ++c;  // this child is dealt with
       }
+      __syncwarp();
     }
   }
 
@@ -677,9 +702,10 @@ size_t tree_verify_workspace_bytes(int B, int n, int V) {
   return (size_t)2 * B * n * chunks * sizeof(verify::Stat);
 }
 
-template <typename T>
+template <typename T, bool DRAFT>
 static cudaError_t verify_launch(verify::Params P, cudaStream_t stream) {
   using namespace verify;
+  constexpr int kPass = kThreads * kPerOf<DRAFT>;
   static std::atomic<int> largest[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -698,15 +724,15 @@ static cudaError_t verify_launch(verify::Params P, cudaStream_t stream) {
   cfg.attrs = attr;
   int most = dev < 64 ? largest[dev].load() : 0;
   if (!most) {
-    e = cudaFuncSetAttribute(walk<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(walk<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDyn);
+    e = cudaFuncSetAttribute(walk<T, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(walk<T, DRAFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDyn);
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = kMaxDyn;
     cfg.numAttrs = 1;
     attr[0].val.clusterDim.x = kMaxCluster;
     cfg.gridDim = dim3(kMaxCluster);
     int fit = 0;
-    if (cudaOccupancyMaxActiveClusters(&fit, walk<T>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&fit, walk<T, DRAFT>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       fit = 0;
     }
@@ -725,7 +751,7 @@ static cudaError_t verify_launch(verify::Params P, cudaStream_t stream) {
   attr[0].val.clusterDim.x = C;
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(C * P.B);
-  return cudaLaunchKernelEx(&cfg, walk<T>, P);
+  return cudaLaunchKernelEx(&cfg, walk<T, DRAFT>, P);
 }
 
 int tree_verify(const TreeVerify& a, void* workspace, cudaStream_t stream, std::string* err) {
@@ -738,9 +764,9 @@ int tree_verify(const TreeVerify& a, void* workspace, cudaStream_t stream, std::
   P.stats = static_cast<verify::Stat*>(workspace);
   P.B = a.B, P.n = a.n, P.V = a.vocab;
   P.chunks = (a.vocab + 8 + verify::kChunk - 1) / verify::kChunk;
-  const cudaError_t e = a.dtype == MK_FP32   ? verify_launch<float>(P, stream)
-                        : a.dtype == MK_BF16 ? verify_launch<__nv_bfloat16>(P, stream)
-                                             : verify_launch<__half>(P, stream);
+  const cudaError_t e = a.dtype == MK_FP32   ? (P.draft ? verify_launch<float, true>(P, stream) : verify_launch<float, false>(P, stream))
+                        : a.dtype == MK_BF16 ? (P.draft ? verify_launch<__nv_bfloat16, true>(P, stream) : verify_launch<__nv_bfloat16, false>(P, stream))
+                                             : (P.draft ? verify_launch<__half, true>(P, stream) : verify_launch<__half, false>(P, stream));
   if (e != cudaSuccess) {
     *err = std::string("tree_verify launch: ") + cudaGetErrorString(e);
     return MK_ERR_CUDA;

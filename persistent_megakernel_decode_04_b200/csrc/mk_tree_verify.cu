@@ -121,19 +121,21 @@ __device__ __forceinline__ int in_use(const Params& P, int b) {
 template <typename T>
 __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kVec = 16 / sizeof(T), kSteps = kChunk / kVec / kStatThreads;
+  constexpr int kVec = 16 / sizeof(T), kSteps = kChunk / kVec / kStatThreads, kStatWarps = kStatThreads / 32;
   const int b = blockIdx.y / P.n, i = blockIdx.y - b * P.n, draft = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nn = in_use(P, b);
-  if (i >= nn) return;
   const float temp = P.temperature ? P.temperature[b] : 1.f;
   float scale = temp;
+  bool wanted = i < nn;
   if (draft) {
-    if (temp == 0.f) return;  // the draft's probabilities are not asked for
+    // the draft's probabilities are asked for where a child was drawn from this row
     scale = P.draft_temperature ? P.draft_temperature[b] : 1.f;
     bool parent = false;
-    for (int c = i + 1 + threadIdx.x; c < nn; c += kStatThreads) parent |= P.parents[(int64_t)b * P.n + c] == i;
-    if (!__syncthreads_or(parent)) return;  // no child was drawn from this row
+    for (int c = i + 1 + lane; c < nn; c += 32) parent |= P.parents[(int64_t)b * P.n + c] == i;
+    wanted = wanted && temp != 0.f && __any_sync(0xffffffffu, parent);
   }
+  if (!wanted) return;
   const float c = 1.44269504088896340736f / scale;
   const T* row = draft ? static_cast<const T*>(P.draft) + b * P.d_seq + i * P.d_node
                        : static_cast<const T*>(P.target) + b * P.t_seq + i * P.t_node;
@@ -151,22 +153,12 @@ __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
       for (int k = 0; k < kVec; ++k) e[k] = j + k >= 0 && j + k < P.V ? row[j + k] : lowest<T>();
     }
   }
-  // NaN takes no part in the maximum; it comes out of the sum
+  // Every thread sums by its own maximum, so that the block waits for its warps only once.  NaN
+  // takes no part in the maximum; it comes out of the sum.
   float own = -INFINITY;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) own = fmaxf(own, max_of<T>(raw[s]));
-  float m = own;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float sm[kStatThreads / 32], ss[kStatThreads / 32];
-  __shared__ int si;
-#pragma unroll
-  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (lane == 0) sm[warp] = m;
-  if (threadIdx.x == 0) si = 0x7fffffff;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kStatThreads / 32; ++k) m = fmaxf(m, sm[k]);
-  const float base = m == -INFINITY ? 0.f : m;
+  const float base = own == -INFINITY ? 0.f : own;
   const uint64_t nb = pack2(-base, -base), cc = pack2(c, c);
   uint64_t acc = 0;  // two sums
 #pragma unroll
@@ -183,25 +175,39 @@ __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
       asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(y));
     }
   }
-  float sum = unpack2(acc).x + unpack2(acc).y;
-  if (own == m) {  // few threads: the lowest place of the maximum
-    int idx = 0x7fffffff;
-#pragma unroll 1
-    for (int s = 0; s < kSteps; ++s) {
-      const int j = j0 + (s * kStatThreads + (int)threadIdx.x) * kVec;
-      for (int k = 0; k < kVec; ++k)
-        if (j + k >= 0 && j + k < P.V && to_f(row[j + k]) == m) idx = min(idx, j + k);
-    }
-    atomicMin(&si, idx);
-  }
+  __shared__ float sm[kStatWarps], ss[kStatWarps];
+  __shared__ int si[kStatWarps];
+  float m = own;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  float sum = (unpack2(acc).x + unpack2(acc).y) * ex2((own - (m == -INFINITY ? 0.f : m)) * c);
 #pragma unroll
   for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) ss[warp] = sum;
+  int idx = 0x7fffffff;
+  if (temp == 0.f) {  // the lowest place of the maximum
+    if (own == m) {
+#pragma unroll 1
+      for (int s = 0; s < kSteps; ++s) {
+        const int j = j0 + (s * kStatThreads + (int)threadIdx.x) * kVec;
+        for (int k = 0; k < kVec; ++k)
+          if (j + k >= 0 && j + k < P.V && to_f(row[j + k]) == m) idx = min(idx, j + k);
+      }
+    }
+    idx = __reduce_min_sync(0xffffffffu, idx);
+  }
+  if (lane == 0) sm[warp] = m, ss[warp] = sum, si[warp] = idx;
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < kStatWarps) {
+    constexpr uint32_t all = (1u << kStatWarps) - 1;
+    m = sm[lane], sum = ss[lane], idx = si[lane];
+    float top = m;
 #pragma unroll
-    for (int k = 1; k < kStatThreads / 32; ++k) sum += ss[k];
-    P.stats[((int64_t)(draft * P.B + b) * P.n + i) * P.chunks + blockIdx.x] = Stat{m, sum, si, 0};
+    for (int off = kStatWarps / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(all, top, off));
+    sum *= ex2((m - (top == -INFINITY ? 0.f : top)) * c);
+#pragma unroll
+    for (int off = kStatWarps / 2; off; off >>= 1) sum += __shfl_xor_sync(all, sum, off);
+    idx = __reduce_min_sync(all, m == top ? idx : 0x7fffffff);
+    if (lane == 0) P.stats[((int64_t)(draft * P.B + b) * P.n + i) * P.chunks + blockIdx.x] = Stat{top, sum, idx, 0};
   }
 }
 

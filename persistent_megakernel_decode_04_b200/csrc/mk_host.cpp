@@ -2178,8 +2178,14 @@ static int check_cache(const mk_cache_shape* s, const void* cache, const int32_t
       s->B > 65535 || s->max_seq > (1 << 26))
     return fail(nullptr, MK_ERR_INVALID_ARG, "bad n_layers, B, max_batch, n_kv_heads, max_seq or head_dim");
   if (reinterpret_cast<uintptr_t>(cache) & 15) return fail(nullptr, MK_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
-  const uintptr_t a = reinterpret_cast<uintptr_t>(lens), c = reinterpret_cast<uintptr_t>(new_lens), size = 4u * s->B;
-  if (a < c + size && c < a + size) return fail(nullptr, MK_ERR_INVALID_ARG, "new_lens must not overlap lens");
+  return MK_OK;
+}
+
+// Every block reads the inputs and one block writes new_lens: that may lie over none of them.
+static int check_new_lens(const int32_t* new_lens, int B, const int32_t* input, int64_t size) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(input), c = reinterpret_cast<uintptr_t>(new_lens);
+  if (a < c + 4u * B && c < a + 4u * size)
+    return fail(nullptr, MK_ERR_INVALID_ARG, "new_lens must not overlap the other arrays");
   return MK_OK;
 }
 
@@ -2188,6 +2194,10 @@ int mk_cache_commit(const mk_cache_shape* shape, void* cache, const int32_t* pat
   if (const int rc = check_cache(shape, cache, lens, new_lens)) return rc;
   if (!path || !n_path) return fail(nullptr, MK_ERR_INVALID_ARG, "NULL operand");
   if (n < 1 || n > MK_MAX_TREE_NODES) return fail(nullptr, MK_ERR_INVALID_ARG, "bad n");
+  const int B = shape->B;
+  for (const int bad : {check_new_lens(new_lens, B, lens, B), check_new_lens(new_lens, B, n_path, B),
+                        check_new_lens(new_lens, B, path, (int64_t)B * n)})
+    if (bad) return bad;
   std::string err;
   const int rc = cache_commit(*shape, cache, path, n, n_path, lens, new_lens, reinterpret_cast<cudaStream_t>(stream), &err);
   if (rc) return fail(nullptr, rc, err);
@@ -2199,6 +2209,8 @@ int mk_cache_reorder(const mk_cache_shape* shape, void* cache, const int32_t* sr
   if (const int rc = check_cache(shape, cache, lens, new_lens)) return rc;
   if (!src) return fail(nullptr, MK_ERR_INVALID_ARG, "NULL operand");
   if (shape->B > MK_MAX_BATCH) return fail(nullptr, MK_ERR_INVALID_ARG, "at most MK_MAX_BATCH sequences");
+  for (const int32_t* input : {lens, src})
+    if (const int bad = check_new_lens(new_lens, shape->B, input, shape->B)) return bad;
   std::string err;
   const int rc = cache_reorder(*shape, cache, src, lens, new_lens, reinterpret_cast<cudaStream_t>(stream), &err);
   if (rc) return fail(nullptr, rc, err);

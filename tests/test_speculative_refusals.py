@@ -90,6 +90,20 @@ def test_cache_operands():
     assert mk._lib.mk_cache_reorder(None, OK, OK, OK, 2 * OK, None) == bad
 
 
+def test_new_lens_over_an_input():
+    bad = mk.MK_ERR_INVALID_ARG
+    far = [OK, 2 * OK, 3 * OK, 4 * OK]  # path, n_path, lens, new_lens
+    for at, size in ((0, 3 * 4 * 4), (1, 12), (2, 12)):
+        for end in (0, size - 4):
+            a = list(far)
+            a[3] = a[at] + end
+            assert mk._lib.mk_cache_commit(cache_shape(), OK, a[0], 4, *a[1:], None) == bad
+            assert "overlap" in mk.mk_last_error()
+    for at in (OK, 2 * OK):  # src, lens
+        for end in (-8, 0, 8):
+            assert mk._lib.mk_cache_reorder(cache_shape(), OK, OK, 2 * OK, at + end, None) == bad
+
+
 def refused(f, *a):
     with pytest.raises(mk.MkError) as e:
         f(*a)

@@ -233,18 +233,19 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 2^y for -1000 <= y <= 0 by a table of 2^(k / 16) and the series of 2^r in the remainder (|r| <=
+// 2^y, y = d c, for -1000 <= y <= 0 by a table of 2^(k / 16) and the series of 2^r in the remainder (|r| <=
 // 1/32; the term behind the fifth is below 1.5e-13).  The method is P. T. P. Tang's, "Table-driven
 // implementation of the exponential function in IEEE floating-point arithmetic", 1989.  The table
 // is kept 16 times, a copy for every other lane, so that lookups meet no bank conflicts (with 256
 // entries once they took half of a pass).  `low`: y is below -1000, the value 0 (told apart in fp32,
-// without a branch: several run side by side).
+// without a branch: several run side by side).  d is a logit minus the row's largest: the largest one's
+// exponential is 1 to the bit, and y as good as d, however small the temperature.
 constexpr int kTable = 16, kCopies = 16;
-__device__ __forceinline__ double exp2_table(double y, bool low, const double* table) {
+__device__ __forceinline__ double exp2_table(double d, double c, bool low, const double* table) {
   constexpr double kMagic = 6755399441055744.0 / kTable;  // 1.5 * 2^52 / 16: the sum's low bits are round(16 y)
-  const double t = y + kMagic;
+  const double t = fma(d, c, kMagic);
   const int k = __double2loint(t);
-  const double r = y - (t - kMagic);
+  const double r = fma(d, c, kMagic - t);
   constexpr double c1 = 0.69314718055994530942, c2 = c1 * c1 / 2, c3 = c2 * c1 / 3, c4 = c3 * c1 / 4, c5 = c4 * c1 / 5;
   double e = table[(k & (kTable - 1)) * kCopies + (threadIdx.x & (kCopies - 1))];
   e = __hiloint2double(__double2hiint(e) + ((k >> 4) << 20), __double2loint(e));
@@ -341,11 +342,11 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     double p = 0.0, q = 0.0;
     if (lt != -INFINITY) {  // (a NaN stays)
       const float mt = S.m[0][par];
-      p = exp2_table(fma((double)lt, tc, -((double)mt * tc)), (lt - mt) * tcf <= -1000.f, S.table);
+      p = exp2_table((double)lt - (double)mt, tc, (lt - mt) * tcf <= -1000.f, S.table);
     }
     if (sampled && ld != -INFINITY) {
       const float md = S.m[1][par];
-      q = exp2_table(fma((double)ld, dc, -((double)md * dc)), (ld - md) * dcf <= -1000.f, S.table);
+      q = exp2_table((double)ld - (double)md, dc, (ld - md) * dcf <= -1000.f, S.table);
     }
     S.p[tid] = p, S.q[tid] = q;
     if (!DRAFT) S.pf[tid] = par >= 0 && par < tid ? (float)p / S.z[0][par] : 0.f;
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       // u q / ZQ < p / ZP without divisions
       const double a = (double)S.u[tid] * (sampled ? q : 1.0) * (double)S.z[0][par];
       const double e = p * (sampled ? (double)S.z[1][par] : 1.0), top = fmax(a, e);
-      S.first[tid] = fabs(a - e) <= (double)kClose * top && top > 0.0 ? 2 : a < e;
+      // (sums that are NaN, as fp32's are at temperatures below 2^-127, settle nothing either)
+      S.first[tid] = !(fabs(a - e) > (double)kClose * top) && top != 0.0 ? 2 : a < e;
     }
     const int x = S.token[tid];
     bool again = x < 0 || x >= V;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
           if (!DRAFT && n_gone > 0) {
             // (fp32 statistics and this sum know what is left to kClose + 6e-8 per term)
             const float p = S.again[c] ? 0.f : S.pf[c], a = S.u[c] * left, top = fmaxf(a, p);
-            first = left < 0.125f || (fabsf(a - p) * left <= (kClose + 6e-8f * n_gone) * top && top > 0.f) ? 2 : a < p;
+            first = !(left >= 0.125f) || (!(fabsf(a - p) * left > (kClose + 6e-8f * n_gone) * top) && top != 0.f) ? 2 : a < p;
           }
           if (first == 2) {
             op = OP_SUMS;  // too close for fp32 statistics: come back with exact ones
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     const bool d_vec = ((reinterpret_cast<uintptr_t>(dp) / sizeof(T)) & 3) == (uintptr_t)lead;
     const int lo = (int)rank * slice - lead, hi = min(V, lo + slice);
     const float mtf = S.m[0][node], mdf = S.m[1][node];
-    const double mp = -((double)mtf * tc), mq = -((double)mdf * dc);
+    const double mp = mtf, mq = mdf;
     const int rounds = op == OP_SUMS ? 0 : S.rounds + (op == OP_REST), n_gone = S.n_gone;
     const double iP = S.iP, iQ = S.iQ;
     auto load4 = [&](const T* row, bool vec, int j, float* x) {
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         for (int k = 0; k < kPer; ++k) v[k] = at_v[k * kThreads];
       } else {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) v[k] = exp2_table(fma((double)tl[k], tc, mp), (tl[k] - mtf) * tcf <= -1000.f, S.table);
+        for (int k = 0; k < kPer; ++k) v[k] = exp2_table((double)tl[k] - mp, tc, (tl[k] - mtf) * tcf <= -1000.f, S.table);
       }
       if (sampled) {
         if (q_from_kept) {
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
           for (int k = 0; k < kPer; ++k) q[k] = at_q[k * kThreads];
         } else {
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) q[k] = exp2_table(fma((double)dl[k], dc, mq), (dl[k] - mdf) * dcf <= -1000.f, S.table);
+          for (int k = 0; k < kPer; ++k) q[k] = exp2_table((double)dl[k] - mq, dc, (dl[k] - mdf) * dcf <= -1000.f, S.table);
           if (P.keep > 1)
 #pragma unroll
             for (int k = 0; k < kPer; ++k) at_q[k * kThreads] = q[k];
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       // the rows once more, as the last pass saw them
       const int rounds = S.rounds;
       const float mtf = S.m[0][S.cur], mdf = S.m[1][S.cur];
-      const double mp = -((double)mtf * tc), mq = -((double)mdf * dc);
+      const double mp = mtf, mq = mdf;
       double v[kPer], sum = 0.0;
       const int j = lo + at / kWarps * kPass + (at % kWarps * 32 + lane) * kPer;
 #pragma unroll
@@ -669,10 +671,10 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
             v[k] = dyn[(at / kWarps * kPer + k) * kThreads + at % kWarps * 32 + lane];
           } else {
             const float tl = to_f(tp[j + k]);
-            v[k] = exp2_table(fma((double)tl, tc, mp), (tl - mtf) * tcf <= -1000.f, S.table);
+            v[k] = exp2_table((double)tl - mp, tc, (tl - mtf) * tcf <= -1000.f, S.table);
             if (rounds > 0) {
               const float dl = to_f(dp[j + k]);
-              const double q = exp2_table(fma((double)dl, dc, mq), (dl - mdf) * dcf <= -1000.f, S.table) * S.iQ;
+              const double q = exp2_table((double)dl - mq, dc, (dl - mdf) * dcf <= -1000.f, S.table) * S.iQ;
               for (int y = 0; y < rounds; ++y) {
                 v[k] = v[k] * (y == 0 ? S.iP : S.iZ[y - 1]) - q;
                 if (v[k] < 0.0) v[k] = 0.0;

@@ -147,6 +147,31 @@ def test_decisions_at_their_border():
     assert call(**x)[1].tolist() == [2, 2, 2]
 
 
+@pytest.mark.parametrize("sampled", [True, False])
+def test_temperatures_near_zero_and_very_high(sampled):
+    # 1e-40: the reciprocal is beyond fp32's range; the law is one-hot at the largest logit
+    x = inputs(6, 9, 2001, "tree", sampled, seed=41)
+    x["temperature"] = torch.tensor([1e-40, 1e-38, 1e-30, 1e-3, 1e3, 1e30])
+    x["draft_temperature"] = torch.tensor([1.0, 1e-40, 0.5, 1e-3, 1e30, 2.0])
+    check(**x)
+
+
+@pytest.mark.parametrize("sampled,V", [(True, 262144), (True, 1 << 20), (False, 1 << 20)])
+def test_the_largest_vocabularies(sampled, V):
+    # a pass's values are kept whole, in part and not at all; more batches than clusters of 16
+    x = inputs(10 if V < 1 << 20 else 2, 4, V, "star", sampled, torch.bfloat16, seed=43)
+    x["u"] = 0.5 + x["u"] / 2  # more rejections
+    check(**x)
+
+
+@pytest.mark.parametrize("n", [33, 256])
+def test_many_certain_siblings_with_little_left(n):
+    # no draft probabilities: what is left of P shrinks to less than an eighth, then further
+    x = inputs(4, n, n + 40, "star", False, seed=n, spread=1.0)
+    x["u"] = 0.6 + 0.4 * x["u"]
+    check(**x)
+
+
 def test_rows_that_are_no_distribution():
     x = inputs(4, 4, 3000, "chain", True, seed=6)
     x["u"][:] = 0.0

@@ -178,13 +178,15 @@ __global__ void qkv_post(const float* Yq, int n, int ct, int t0, const float2* r
 
 // The same for row (b, i) of a step over drafted trees: node i of sequence b.  It is rotated to
 // position lens[b] + depth (its ancestors' count), and its K and V go to cache row lens[b] + i.
-// Nodes that do not fit the cache write nothing to it.
-__global__ void tree_qkv_post(const float* Yq, int n, const int32_t* parents, const int32_t* lens, const float2* rope,
+// Nodes that are not in use or do not fit the cache write nothing to it.
+__global__ void tree_qkv_post(const float* Yq, int n, const int32_t* parents, const int32_t* n_nodes,
+                              const int32_t* lens, const float2* rope,
                               float* Q, uint16_t* kv, int layer, int nq, int nkv, int D, int max_seq,
                               int max_batch) {
   __shared__ int s_pos;
   const int row = blockIdx.x, b = row / n, i = row % n;
   const int len = min(max(lens[b], 0), max_seq), at = len + i;
+  const bool keep = at < max_seq && (!n_nodes || i < n_nodes[b]);
   if (threadIdx.x == 0) {
     int depth = 0;
     for (int c = i; depth < i; ++depth) {
@@ -213,9 +215,9 @@ __global__ void tree_qkv_post(const float* Yq, int n, const int32_t* parents, co
       const int dim = hi ? k + half : k;
       if (rr < G * D)
         Q[(size_t)row * nq * D + (size_t)(grp * G + rr / D) * D + dim] = outv;
-      else if (at < max_seq)
+      else if (keep)
         kv[((size_t)layer * 2 + 0) * kv_layer + cell + dim] = f2bf(outv);
-    } else if (at < max_seq) {
+    } else if (keep) {
       kv[((size_t)layer * 2 + 1) * kv_layer + cell + rr - (G + 1) * D] = f2bf(v);
     }
   }
@@ -390,7 +392,7 @@ int run_tree_forward(const PrefillParams& p, const int32_t* tokens, const int32_
     gemm(p.XN, reinterpret_cast<const uint16_t*>(p.arena + lo.qkv), p.Y, rows, NQKV, H, NQKV, s, p.blocked);
     if (p.qk_norm)
       pf::qk_norm<<<rows, 256, 0, s>>>(p.Y, reinterpret_cast<const uint16_t*>(p.arena + lo.qkn), nq, nkv, D, p.eps);
-    pf::tree_qkv_post<<<rows, 256, 0, s>>>(p.Y, n, parents, lens, p.rope, p.Q, p.kv, l, nq, nkv, D, p.max_seq, p.max_batch);
+    pf::tree_qkv_post<<<rows, 256, 0, s>>>(p.Y, n, parents, n_nodes, lens, p.rope, p.Q, p.kv, l, nq, nkv, D, p.max_seq, p.max_batch);
     const int rc = tree_attention(t, p.Q, p.kv + 2 * l * plane, p.kv + (2 * l + 1) * plane, p.O, parents, n_nodes, lens,
                                   p.attn_scale, n_sms, s, err);
     if (rc) return rc;

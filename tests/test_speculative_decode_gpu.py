@@ -152,3 +152,80 @@ def test_tree_forward_at_the_caches_end():
     with pytest.raises(mk.MkError):
         m.tree_forward(i32([[0] * 40] * 2), i32([[-1] * 40] * 2), i32([0, 0]))  # 80 rows: scratch for 64
     m.close()
+
+
+def test_nodes_not_in_use_leave_the_cache_alone():
+    w, m = model(mi.TINY, 4, 48)
+    prompts = np.stack([mi.prompt(4, b, 20, w.shape.vocab) for b in range(4)])
+    m.prefill(i32(prompts))
+    before = m.kv_view().clone()
+    toks = i32([[1, 2, 3, 4, 5, 6]] * 3)
+    par = i32([[-1, 0, 0, 1, 2, 3]] * 3)
+    use = [2, 0, 99]
+    got = m.tree_forward(toks, par, i32([20, 7, 20]), i32(use))
+    after = m.kv_view().clone()
+    for b, ln, nn in ((0, 20, 2), (1, 7, 0), (2, 20, 6), (3, 20, 0)):
+        assert torch.equal(after[:, :, b, :, :ln], before[:, :, b, :, :ln])
+        assert torch.equal(after[:, :, b, :, ln + nn:], before[:, :, b, :, ln + nn:])
+    every = m.tree_forward(toks, par, i32([20, 7, 20]))
+    for b, nn in ((0, 2), (2, 6)):
+        assert torch.equal(got[b, :nn], every[b, :nn])
+    m.close()
+
+
+def test_a_whole_step_replayed_from_a_graph():
+    """Forward, verification and commit captured once, then replayed with other drafts: what the
+    same calls give one by one."""
+    w, m = model(mi.TINY, 2, 96)
+    B, n, V, T = 2, 6, w.shape.vocab, 10
+    prompts = np.stack([mi.prompt(8, b, T, V) for b in range(B)])
+    m.prefill(i32(prompts))
+    start = m.kv_view().clone()
+    rng = np.random.default_rng(3)
+    tokens, parents = i32(np.zeros((B, n))), i32(np.tile([-1, 0, 0, 1, 2, 4], (B, 1)))
+    lens, new_lens = i32([T] * B), i32([0] * B)
+    u, r = torch.zeros(B, n, device=DEV), torch.zeros(B, device=DEV)
+    temperature = torch.full((B,), 0.2, device=DEV)
+    path, n_path, nxt = i32(np.zeros((B, n))), i32([0] * B), i32([0] * B)
+    logits = torch.empty(B, n, V, device=DEV)
+    ws = torch.empty(mk.mk_tree_verify_workspace_bytes(B, n, V), dtype=torch.uint8, device=DEV)
+    stream = torch.cuda.Stream()
+
+    def step():
+        mk.mk_tree_forward(m.ctx, tokens, parents, None, lens, B, n, m.kv, logits, stream)
+        mk.mk_tree_verify(logits, None, tokens, parents, None, u, r, temperature, None, path, n_path, nxt, ws, stream)
+        mk.mk_cache_commit(m.kv_view(), path, n_path, lens, new_lens, stream)
+
+    drafts = []
+    for _ in range(4):
+        t = rng.integers(0, V, (B, n)).astype(np.int32)
+        drafts.append((t, torch.rand(B, n, device=DEV) * 0.05, torch.rand(B, device=DEV)))
+
+    def run(go):
+        m.kv_view().copy_(start)
+        lens.fill_(T)
+        out = []
+        for t, uu, rr in drafts:
+            tokens.copy_(torch.from_numpy(t))
+            u.copy_(uu)
+            r.copy_(rr)
+            torch.cuda.synchronize()
+            go()
+            stream.synchronize()
+            out += [path.clone(), n_path.clone(), nxt.clone(), new_lens.clone(), logits.clone()]
+            lens.copy_(new_lens)
+        return out + [m.kv_view().clone()]
+
+    one_by_one = run(step)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+        step()
+
+    def replay():
+        with torch.cuda.stream(stream):
+            graph.replay()
+
+    for a, b in zip(one_by_one, run(replay)):
+        assert torch.equal(a, b)
+    assert mk.mk_tree_attention_status() == mk.MK_OK
+    m.close()

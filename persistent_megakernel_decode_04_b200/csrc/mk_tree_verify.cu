@@ -16,7 +16,7 @@
 //
 // Bound: the walk's latency.  A pass over a row of 128255 words by 8 blocks takes 6 to 9 us, a third
 // of it exchange and control, the rest fp64 arithmetic at half its rate (16 blocks: 4 to 5).  16
-// sequences x 9 nodes of that size (bf16, sampled drafts) take 68 us, of which row_stats 15 and the
+// sequences x 9 nodes of that size (bf16, sampled drafts) take 65 us, of which row_stats 15 and the
 // longest walk nearly all the rest; one chain of 5 (fp32, 128256 words) 16 us; 4 x 26 nodes of 65536
 // words without a draft 20 us.
 //
@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -50,7 +51,7 @@ constexpr float kClose = 1e-5f;
 // four need few enough registers for row_stats's blocks beside the walk's
 template <bool DRAFT>
 constexpr int kPerOf = DRAFT ? 8 : 4;
-constexpr int kMaxDyn = 192 * 1024;  // walk: dynamic shared memory
+constexpr int kMaxDyn = 204 * 1024;  // walk: dynamic shared memory, beside 21 KB of Ctl
 
 struct Stat {  // of one row's chunk
   float m, s;
@@ -65,7 +66,9 @@ struct Params {
   int32_t *path, *n_path, *next_token;
   Stat* stats;  // [target | draft][B][n][chunks]
   int B, n, V, chunks;
-  int keep;  // walk: a pass keeps its values in shared memory: 0 no, 1 of the target, 2 and of the draft
+  // walk: whether a pass keeps what it has of P in shared memory, and of how many of its steps the
+  // draft's exponentials
+  int keep, q_steps;
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   const int room = (slice + kPass - 1) / kPass * kPass;
   double* const kept_v = dyn + tid;
   double* const kept_q = kept_v + room;
-  double* const piece = dyn + P.keep * room;
+  double* const piece = dyn + P.keep * room + P.q_steps * kPass;
   __syncwarp();
   for (;;) {
     if (warp == 0) {
@@ -488,7 +491,6 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     // Rejections one after another start from what the pass before kept, not from the logits.
     const bool store = sampled && P.keep > 0;
     const bool from_kept = store && op == OP_REST && S.kept == rounds - 1;
-    const bool q_from_kept = from_kept && P.keep > 1;
     const double scale = rounds > 1 ? S.iZ[rounds > 1 ? rounds - 2 : 0] : iP;
     double sv = 0.0, sq = 0.0;
     float tl[kPer], dl[kPer] = {};
@@ -497,6 +499,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       double v[kPer], q[kPer];
       double* const at_v = kept_v + s * kPass;
       double* const at_q = kept_q + s * kPass;
+      const bool keep_q = store && s < P.q_steps, q_from_kept = from_kept && keep_q;
       if (!from_kept)
 #pragma unroll
         for (int k = 0; k < kPer; k += 4) load4(tp, true, j + k, tl + k);
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         } else {
 #pragma unroll
           for (int k = 0; k < kPer; ++k) q[k] = exp2_table((double)dl[k] - mq, dc, (dl[k] - mdf) * dcf <= -1000.f, S.table);
-          if (P.keep > 1)
+          if (keep_q)
 #pragma unroll
             for (int k = 0; k < kPer; ++k) at_q[k * kThreads] = q[k];
         }
@@ -761,8 +764,10 @@ static cudaError_t verify_launch(verify::Params P, cudaStream_t stream) {
   // shared memory as the kernel lays it out
   const int slice = ((P.V + 3 + C - 1) / C + 3) & ~3, steps = (slice + kPass - 1) / kPass;
   const size_t row = (size_t)steps * kPass * sizeof(double), pieces = (size_t)steps * kWarps * sizeof(double);
-  P.keep = !P.draft ? 0 : 2 * row + pieces <= kMaxDyn ? 2 : row + pieces <= kMaxDyn ? 1 : 0;
-  cfg.dynamicSmemBytes = P.keep * row + pieces;
+  const size_t step = kPass * sizeof(double);
+  P.keep = P.draft && row + pieces <= kMaxDyn;
+  P.q_steps = P.keep ? (int)std::min<size_t>(steps, (kMaxDyn - row - pieces) / step) : 0;
+  cfg.dynamicSmemBytes = P.keep * row + P.q_steps * step + pieces;
   if (cfg.dynamicSmemBytes > kMaxDyn) return cudaErrorInvalidValue;
   attr[0].val.clusterDim.x = C;
   cfg.numAttrs = 2;

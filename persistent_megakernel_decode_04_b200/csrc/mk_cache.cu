@@ -25,8 +25,11 @@ struct Params {
 // path[j] >= j and both grow, so a row is never written before a later copy has read it as long
 // as the copies of a plane go in order: a warp takes a plane's 32 / row copies at a time, several
 // such groups' loads before their stores.  Rows of 256 bytes far apart: 16 sequences' paths through
-// 64-node trees (32 layers, 32 heads of 128) take 23 us, 4.6 TB/s; one sequence's (8 heads) 3 us.
-__global__ void __launch_bounds__(kThreads) commit(const Params P) {
+// 64-node trees (32 layers, 32 heads of 128) take 13 us, the rate of a plain copy; one sequence's
+// (8 heads) 2.4 us.  Six blocks per SM, all resident at once, read the path once each: with a block for
+// every 8 planes, eight groups in flight and so three blocks per SM it took 23 us.
+constexpr int kCommitBlocks = 6;
+__global__ void __launch_bounds__(kThreads, kCommitBlocks) commit(const Params P) {
   __shared__ int16_t path[kMaxNodes];
   __shared__ int s_count, s_first;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -58,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) commit(const Params P) {
   const int count = s_count, first = s_first;  // copies first .. count - 1 move something
   const int per = 32 / P.row, r = lane / P.row, c = lane - r * P.row;
   const int planes = P.layers * 2 * P.hkv;
-  constexpr int kDeep = 8;
+  constexpr int kDeep = 4;
   for (int x = blockIdx.x * (kThreads / 32) + warp; x < planes; x += gridDim.x * (kThreads / 32)) {
     const int h = x % P.hkv, lk = x / P.hkv;
     uint4* p = P.base + (lk >> 1) * P.layer + (lk & 1) * P.kv + b * P.seq + h * P.head + (int64_t)len * P.row + c;
@@ -179,7 +182,8 @@ int cache_commit(const mk_cache_shape& s, void* cache, const int32_t* path, int 
   cache::Params P = cache::params(s, cache, lens, new_lens);
   P.path = path, P.n_path = n_path, P.n = n;
   const int planes = s.n_layers * 2 * s.n_kv_heads, warps = cache::kThreads / 32;
-  cache::commit<<<dim3((planes + warps - 1) / warps, s.B), cache::kThreads, 0, stream>>>(P);
+  const int all = (planes + warps - 1) / warps, want = (cache::kCommitBlocks * n_sms_now() + s.B - 1) / s.B;
+  cache::commit<<<dim3(all < want ? all : want, s.B), cache::kThreads, 0, stream>>>(P);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     *err = std::string("cache commit launch: ") + cudaGetErrorString(e);

@@ -884,10 +884,13 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params&
   const int64_t units = (int64_t)B * P.hkv * P.units;
   if (units > (1 << 27)) return cudaErrorInvalidValue;
   // Blocks that share a unit's keys: the split with the least estimated time.  A block takes as long
-  // as 8 tiles for its start and end, and half as long again where two share an SM; more clusters
-  // than run at once go in turns (a few more than one turn's cost little).  Measured, us for 1, 2, 4,
-  // 8, 16 blocks: 8 units of 4122 rows 53 35 25 19 18; 16 units of 2056 rows 31 23 17 14 23; 64 units
-  // of 16448 rows 192 107 82 110 150; 512 units of 4352 rows 136 147 180 270 577.
+  // as 7.3 tiles (0.7 us each) for its start and end, a cluster's exchange some more, and all that half
+  // as long again where two share an SM; more clusters than run at once go in turns (a few more than
+  // one turn's cost little).  Measured, us for 1, 2, 4, 8, 16 blocks: 8 units of 144 rows 6.5 7.2 7.2 7.5
+  // 8.2; 8 of 1040 rows 16 12 9.2 8.2 9.9; 8 of 4122 rows 53 35 25 19 18; 16 of 2056 rows 31 23 17 14 23;
+  // 32 of 1040 rows 16 13 10 12 25; 128 of 1040 rows 17.8 18.3 24 36 78; 64 of 16448 rows 192 107 82 110
+  // 150; 512 of 4352 rows 136 147 180 270 577.
+  constexpr double exchange[5] = {0.0, 2.1, 2.7, 3.5, 6.0};
   const double tiles = (double)P.max_seq / kKeys;
   int C = 1;
   double best = 0.0;
@@ -895,7 +898,7 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params&
     const int at_once = k == 0 ? (cfg.dynamicSmemBytes > 100 * 1024 ? 1 : 2) * n_sms : fit[k - 1];
     if (at_once < 1) continue;
     const double turns = (double)units / at_once;
-    const double t = (8.0 + tiles / (1 << k)) * (units << k > n_sms ? 1.5 : 1.0) *
+    const double t = (7.3 + exchange[k] + tiles / (1 << k)) * (units << k > n_sms ? 1.5 : 1.0) *
                      (turns <= 1.0 ? 1.0 : turns <= 1.1 ? turns : ceil(turns));
     if (k == 0 || t < best) best = t, C = 1 << k;
   }

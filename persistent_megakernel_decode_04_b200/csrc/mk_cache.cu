@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "mk_internal.h"
+#include "mk_ptx.cuh"
 
 namespace mk {
 namespace cache {
@@ -30,6 +31,7 @@ struct Params {
 // every 8 planes, eight groups in flight and so three blocks per SM it took 23 us.
 constexpr int kCommitBlocks = 6;
 __global__ void __launch_bounds__(kThreads, kCommitBlocks) commit(const Params P) {
+  griddep_wait();
   __shared__ int16_t path[kMaxNodes];
   __shared__ int s_count, s_first;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -119,6 +121,7 @@ __device__ __forceinline__ void move_places(const Params& P, V* p, int64_t at, i
 }
 
 __global__ void __launch_bounds__(kThreads, 3) reorder(const Params P) {
+  griddep_wait();
   __shared__ int from[kB], upto[kB];   // sequences to read, and how many pieces of each
   __shared__ uint32_t to[kB];          // the sequences that take them
   __shared__ int s_distinct, s_most;
@@ -183,8 +186,7 @@ int cache_commit(const mk_cache_shape& s, void* cache, const int32_t* path, int 
   P.path = path, P.n_path = n_path, P.n = n;
   const int planes = s.n_layers * 2 * s.n_kv_heads, warps = cache::kThreads / 32;
   const int all = (planes + warps - 1) / warps, want = (cache::kCommitBlocks * n_sms_now() + s.B - 1) / s.B;
-  cache::commit<<<dim3(all < want ? all : want, s.B), cache::kThreads, 0, stream>>>(P);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(cache::commit, dim3(all < want ? all : want, s.B), cache::kThreads, stream, P);
   if (e != cudaSuccess) {
     *err = std::string("cache commit launch: ") + cudaGetErrorString(e);
     return MK_ERR_CUDA;
@@ -201,8 +203,7 @@ int cache_reorder(const mk_cache_shape& s, void* cache, const int32_t* src, cons
   const int64_t pieces = (int64_t)s.max_seq * P.row;
   const int y = planes < 65535 ? planes : 65535, want = (8 * n_sms_now() + y - 1) / y;
   const int64_t most = (pieces + cache::kThreads - 1) / cache::kThreads;
-  cache::reorder<<<dim3((unsigned)(want < most ? want : most), y), cache::kThreads, 0, stream>>>(P);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(cache::reorder, dim3((unsigned)(want < most ? want : most), y), cache::kThreads, stream, P);
   if (e != cudaSuccess) {
     *err = std::string("cache reorder launch: ") + cudaGetErrorString(e);
     return MK_ERR_CUDA;

@@ -1,8 +1,10 @@
 // mk_ptx.cuh -- thin inline-PTX wrappers for sm_100a used by the library's kernels:
 // shared-memory mbarriers, bulk and tensor TMA copies, gpu-scope acquire/release and
-// the global timer.  Each wrapper is one PTX instruction (ISA 8.x forms).
+// the global timer.  Each wrapper is one PTX instruction (ISA 8.x forms).  At the end, launches whose
+// start overlaps the end of the kernel before.
 #pragma once
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace mk {
@@ -309,5 +311,24 @@ __device__ __forceinline__ uint64_t tc_smem_desc(uint32_t saddr, uint32_t lbo, u
 
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// A kernel launched early may start before the one ahead of it in the stream has ended: until this
+// returns it reads and writes no memory that others use.  Every block waits (then the kernel after
+// it, which waits for this one, follows all that ran before).
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename Params>
+inline cudaError_t launch_early(void (*kernel)(Params), dim3 grid, int threads, cudaStream_t stream, const Params& p) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 }  // namespace mk

@@ -431,6 +431,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
 
+  griddep_wait();  // inputs and outputs belong to what ran before until here
+
   const int unit = blockIdx.x / C, head = unit / P.units;
   const int b = head / P.hkv, h = head - b * P.hkv;
   const int first = (unit - head * P.units) * P.nt;  // first node of the block's row tile
@@ -868,7 +870,7 @@ static cudaError_t clusters_at_once(cudaLaunchConfig_t& cfg, cudaLaunchAttribute
 
 template <int D, bool FP16, bool WIDE>
 static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params& P, int B, int n_sms, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
@@ -877,6 +879,8 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params&
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   int fit[4];
   const cudaError_t e = clusters_at_once<D, FP16, WIDE>(cfg, attr, fit);
   if (e != cudaSuccess) return e;
@@ -904,6 +908,7 @@ static cudaError_t launch(const CUtensorMap& mk_, const CUtensorMap& mv, Params&
   }
   attr[0].val.clusterDim.x = C;
   cfg.gridDim = dim3((unsigned)(units * C));
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, tree_attention<D, FP16, WIDE>, mk_, mv, P);
 }
 

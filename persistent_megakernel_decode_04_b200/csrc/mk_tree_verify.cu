@@ -131,7 +131,8 @@ __device__ __forceinline__ int in_use(const Params& P, int b) {
 // Chunks are cut at 16-byte borders, counted from the last border before the row.
 template <typename T>
 __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  griddep_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (all that ran before is complete)
   constexpr int kVec = 16 / sizeof(T), kSteps = kChunk / kVec / kStatThreads, kStatWarps = kStatThreads / 32;
   const int b = blockIdx.y / P.n, i = blockIdx.y - b * P.n, draft = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   }
   if (tid < kTable * kCopies && !greedy) S.table[tid] = exp2(tid / kCopies / (double)kTable);
   cluster_sync();  // also: every block of the cluster has started
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // row_stats is done
+  griddep_wait();  // row_stats is done
   // a row's statistics from its chunks, a warp per row
 #pragma unroll 1
   for (int x = warp; x < nn * (sampled ? 2 : 1); x += kWarps) {
@@ -729,8 +730,7 @@ static cudaError_t verify_launch(verify::Params P, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  row_stats<T><<<dim3(P.chunks, P.B * P.n, P.draft ? 2 : 1), kStatThreads, 0, stream>>>(P);
-  e = cudaGetLastError();
+  e = launch_early(row_stats<T>, dim3(P.chunks, P.B * P.n, P.draft ? 2 : 1), kStatThreads, stream, P);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -19,10 +19,10 @@
 // the ancestor bits of every node, and V tiles that end the sequence.
 //
 // Bound.  With few rows per key memory: 16 sequences x 13 nodes over up to 1280 rows (32 KV heads of
-// 128) take 44 us, 4.6 TB/s.  With many the chain of a tile, scores - softmax - P - product: 8 x 256
+// 128) take 43 us, 4.7 TB/s.  With many the chain of a tile, scores - softmax - P - product: 8 x 256
 // nodes over 4096 rows (32 / 4 heads of 64) take 133 us, 550 TFLOP/s, with the exponential unit busy
 // for less than half of the time and the tensor cores for a third; 4 x 64 nodes over up to 32768 rows
-// (32 / 8 heads of 128) 118 us, 770 TFLOP/s for the rows that are there.  5 nodes over 551 rows: 8.2 us,
+// (32 / 8 heads of 128) 120 us, 760 TFLOP/s for the rows that are there.  5 nodes over 551 rows: 7.5 us,
 // of which the loads' and the cluster's latencies are nearly all.
 //
 // The keys of a (sequence, KV head, row tile) unit are split over a thread-block cluster, whose
@@ -431,17 +431,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
 
-  griddep_wait();  // inputs and outputs belong to what ran before until here
-
   const int unit = blockIdx.x / C, head = unit / P.units;
   const int b = head / P.hkv, h = head - b * P.hkv;
   const int first = (unit - head * P.units) * P.nt;  // first node of the block's row tile
-  int len = P.lens[b], nn = P.n_nodes ? P.n_nodes[b] : P.n;
   const int row = tid & 127;  // of a softmax thread
   const int local = (int)(row * P.inv_g >> 16);
 
-  // ---- start: whatever does not need the lengths first ----
-  int parent = -1;
+  // ---- start: whatever needs no input first ----
   if (warp == kTmaWarp) {
     if (lane == 0) {
       prefetch_tensormap(&map_k);
@@ -466,7 +462,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == kMmaWarp) {
     tc_alloc(&S.tmem, Ge::kCols);
     tc_relinquish();
-  } else if (warp == kHelper) {
+  }
+  griddep_wait();  // inputs and outputs belong to what ran before until here
+  int len = P.lens[b], nn = P.n_nodes ? P.n_nodes[b] : P.n, parent = -1;
+  if (warp == kHelper) {
     if (lane < P.n) parent = P.parents[(int64_t)b * P.n + lane];
   } else if (warp < kSoft) {
     // Q rows into the swizzled tile: 16-byte piece c of row r goes to piece c ^ (r % 8).  Rows of
@@ -746,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) mbar_arrive(&S.p_full[j & 1]);
     }
     // ---- the end: every product is done, Q and the ring are read out ----
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel may take the places that fall free
     if (T > 0) ok = ok && wait_warp(&S.o_full, 0, P, S);
     tc_fence_after();
     if (C > 1) {  // every block's Q and ring are read out

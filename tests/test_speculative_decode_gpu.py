@@ -229,3 +229,60 @@ def test_a_whole_step_replayed_from_a_graph():
         assert torch.equal(a, b)
     assert mk.mk_tree_attention_status() == mk.MK_OK
     m.close()
+
+
+def test_two_streams_forked_and_joined_in_a_graph():
+    """Attention of one stream's data beside a commit and a verification on another, joined before a
+    reorder that needs both; copies and fills ahead of the kernels; replayed several times."""
+    g = torch.Generator().manual_seed(11)
+    B, n, hq, hkv, d, S, V = 2, 9, 8, 2, 64, 200, 3001
+    q = torch.randn(B, n, hq, d, generator=g).bfloat16().to(DEV)
+    src_kv = torch.randn(2, 2, B, hkv, S, d, generator=g).bfloat16().to(DEV)
+    kv, o = torch.empty_like(src_kv), torch.empty_like(q)
+    other = src_kv.flip(4).contiguous()
+    target = torch.randn(B, n, V, generator=g).to(DEV)
+    parents = i32(np.tile([-1, 0, 0, 1, 1, 2, 3, 3, 6], (B, 1)))
+    tokens = target[:, :1].argsort(-1, descending=True)[:, 0, :n].to(torch.int32).contiguous()
+    lens, new_lens, third, fourth = i32([150, 77]), i32([0, 0]), i32([0, 0]), i32([0, 0])
+    u, r = torch.full((B, n), 1e-4, device=DEV), torch.tensor([0.2, 0.7], device=DEV)
+    path, n_path, nxt = i32(np.zeros((B, n))), i32([0] * B), i32([0] * B)
+    ws = torch.empty(mk.mk_tree_verify_workspace_bytes(B, n, V), dtype=torch.uint8, device=DEV)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def calls():
+        kv.copy_(src_kv)
+        o.zero_()
+        fork, join = torch.cuda.Event(), torch.cuda.Event()
+        fork.record(one)
+        two.wait_event(fork)
+        mk.mk_tree_attention(q, kv[0, 0], kv[0, 1], o, parents, None, lens, 0.125, one)
+        with torch.cuda.stream(two):
+            path.fill_(-7)
+            mk.mk_tree_verify(target, None, tokens, parents, None, u, r, None, None, path, n_path, nxt, ws, two)
+            mk.mk_cache_commit(other, path, n_path, lens, new_lens, two)
+        join.record(two)
+        one.wait_event(join)
+        mk.mk_cache_commit(kv, path, n_path, lens, third, one)
+        mk.mk_cache_reorder(kv, i32_src, third, fourth, one)
+
+    i32_src = i32([1, 0])
+    kept = other.clone()
+    with torch.cuda.stream(one):
+        calls()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (o, path, n_path, nxt, new_lens, third, fourth, kv, other)]
+    assert int(n_path.min()) > 1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(one), torch.cuda.graph(graph, stream=one):
+        calls()
+    for _ in range(3):
+        other.copy_(kept)
+        for t in (o, path, n_path, nxt, new_lens, third, fourth, kv):
+            t.fill_(3)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(one):
+            graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, (o, path, n_path, nxt, new_lens, third, fourth, kv, other)):
+            assert torch.equal(a, b)
+    assert mk.mk_tree_attention_status() == mk.MK_OK

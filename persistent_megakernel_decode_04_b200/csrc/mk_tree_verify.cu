@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
     wanted = wanted && temp != 0.f && __any_sync(0xffffffffu, parent);
   }
   if (!wanted) return;
-  const float c = 1.44269504088896340736f / scale;
+  const float c = 1.44269504088896340736f / (temp == 0.f ? 1.f : scale);  // (at 0 the sum shows NaN and infinities)
   const T* row = draft ? static_cast<const T*>(P.draft) + b * P.d_seq + i * P.d_node
                        : static_cast<const T*>(P.target) + b * P.t_seq + i * P.t_node;
   const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));  // elements since the last border
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
     float x[kVec];
     floats_of<T>(raw[s], x);
 #pragma unroll
-    for (int k = 0; k < kVec; k += 2) {  // exp2((x - base) c); at temperature 0 the sum is not used
+    for (int k = 0; k < kVec; k += 2) {  // exp2((x - base) c)
       uint64_t y = pack2(x[k], x[k + 1]);
       asm("add.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(nb));
       asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(cc));
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   const float temp = P.temperature ? P.temperature[b] : 1.f;
   const bool greedy = temp == 0.f, sampled = DRAFT && !greedy;
   const double kLog2e = 1.44269504088896340736;
-  const double tc = kLog2e / (double)temp;
+  const double tc = kLog2e / (greedy ? 1.0 : (double)temp);
   const double dc = sampled ? kLog2e / (double)(P.draft_temperature ? P.draft_temperature[b] : 1.f) : 0.0;
   const float tcf = (float)tc, dcf = (float)dc;
   const T* target = static_cast<const T*>(P.target) + b * P.t_seq;
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     idx = __reduce_min_sync(0xffffffffu, idx);
     if (lane == 0) {
       S.m[d][i] = top, S.z[d][i] = z;
-      if (!d) S.idx[i] = idx;
+      if (!d) S.idx[i] = z > 0.f && z < INFINITY ? idx : -1;  // (else no distribution)
     }
   }
   __syncthreads();
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     P.n_path[b] = depth;
   }
   if (greedy || nn == 0) {
-    if (tid == 0 && rank == 0) P.next_token[b] = nn > 0 && S.idx[S.cur] < V ? S.idx[S.cur] : -1;
+    if (tid == 0 && rank == 0) P.next_token[b] = nn > 0 ? S.idx[S.cur] : -1;
   } else if (warp == 0) {
     const int slot = (turn - 1) & 1;
     const double total = S.total, want = P.r[b] > 0.f ? (double)P.r[b] * total : 0.0;

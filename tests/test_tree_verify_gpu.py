@@ -185,6 +185,24 @@ def test_rows_that_are_no_distribution():
     assert nxt.tolist()[:3] == [-1, -1, -1] and 0 <= int(nxt[3]) < 100
 
 
+@pytest.mark.parametrize("sampled", [True, False])
+def test_rows_that_are_no_distribution_at_temperature_zero(sampled):
+    x = inputs(6, 5, 3000, "chain", sampled, seed=7)
+    x["tokens"][:, 1:] = x["target"].argmax(-1)[:, :-1]  # every draft is the greedy one
+    x["temperature"] = torch.zeros(6)
+    x["target"][0, 0, 2000] = float("nan")
+    x["target"][1, 1, :] = float("-inf")
+    x["target"][2, 2, 5] = float("inf")
+    x["tokens"][2, 3] = 5
+    x["target"][3, 3, :] = float("nan")
+    x["tokens"][3, 4] = 2 ** 31 - 1
+    x["target"][4, :, 100:] = float("-inf")
+    x["tokens"][4, 1:] = x["target"][4].argmax(-1)[:-1]
+    assert check(**x) == [1, 2, 3, 4, 5, 5]
+    path, n_path, nxt = call(**x)
+    assert nxt.tolist()[:4] == [-1] * 4
+
+
 def test_odd_strides_and_unaligned_rows():
     x = inputs(2, 5, 1000, "tree", True, torch.bfloat16, seed=7)
     whole = {}

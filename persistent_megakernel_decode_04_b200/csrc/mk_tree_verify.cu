@@ -16,8 +16,8 @@
 //
 // Bound: the walk's latency.  A pass over a row of 128255 words by 8 blocks takes 6 to 9 us, a third
 // of it exchange and control, the rest fp64 arithmetic at half its rate (16 blocks: 4 to 5).  16
-// sequences x 9 nodes of that size (bf16, sampled drafts) take 65 us, of which row_stats 15 and the
-// longest walk nearly all the rest; one chain of 5 (fp32, 128256 words) 16 us; 4 x 26 nodes of 65536
+// sequences x 9 nodes of that size (bf16, sampled drafts) take 67 us, of which row_stats 15 and the
+// longest walk nearly all the rest; one chain of 5 (fp32, 128256 words) 17 us; 4 x 26 nodes of 65536
 // words without a draft 20 us.
 //
 // Precision.  A draw from 1e5 words by cumulative sums meets a border within 1e-7 in about every
@@ -232,6 +232,9 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void st_peer_f64(uint32_t addr, double x) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(x) : "memory");
 }
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -257,7 +260,7 @@ __device__ __forceinline__ double exp2_table(double d, double c, bool low, const
   return low ? 0.0 : e;
 }
 
-enum Op { OP_DONE, OP_SUMS, OP_REST, OP_AGAIN };
+enum Op { OP_DONE, OP_SUMS, OP_REST, OP_AGAIN, OP_APART };
 
 struct Ctl {
   double table[kTable * kCopies];
@@ -273,6 +276,10 @@ struct Ctl {
   uint8_t first[kMaxNodes];        // a child's answer when it is the first one asked: 0, 1, 2 (too close)
   uint8_t again[kMaxNodes];        // a child whose token an earlier sibling had, or outside the vocabulary
   int op, cur, rounds, n_gone;
+  // What each block is about to do, by turns.  They decide alike from the same numbers; where those
+  // changed under the call (inputs or a workspace that something else writes meanwhile) the blocks part
+  // at the next barrier instead of waiting for one another there for ever.
+  uint32_t step, steps[2][kMaxCluster];
   int kept;  // rejections that the kept values stand for (0: the exponentials), -1: none are kept
 };
 
@@ -375,6 +382,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   int cur = 0, depth = nn > 0 ? 1 : 0, c = 1;  // warp 0's
   bool exact = false;                          // iP, iQ are the current node's
   bool summed = false;                         // `piece` holds the current P
+  bool apart = false;                          // the blocks' decisions differ
   float left = 1.f;                            // without draft: what of P is not gone,
   double left_exact = 1.0;                     // and the same from exact sums
   if (tid == 0) S.rounds = S.n_gone = 0, S.kept = -1;
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     if (warp == 0) {
       int op = OP_DONE;
       int rounds = S.rounds, n_gone = S.n_gone;
-      for (;;) {
+      while (!apart) {
         // the current node's next child from c on
         uint32_t kids = 0;
         int base = c;
@@ -448,16 +456,18 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         ++c;
       }
       if (op == OP_DONE && !greedy && nn > 0 && !summed) op = rounds > 0 ? OP_AGAIN : OP_SUMS;
+      if (apart) op = OP_APART;
       __syncwarp();
       if (lane == 0) {
         S.rounds = rounds, S.n_gone = n_gone;
         S.op = op;
         S.cur = cur;
+        S.step = 1u << 31 | (uint32_t)op << 28 | rounds << 18 | cur << 9 | c;
       }
     }
     __syncthreads();
     const int op = S.op;
-    if (op == OP_DONE) break;
+    if (op == OP_DONE || op == OP_APART) break;
     // ---- a pass over the current node's rows: this block's slice, kPer elements per thread and step.
     // OP_SUMS: sums of the exponentials (without the tokens that are gone: also what is drawn
     // from when nothing was rejected).  OP_REST: the sum of the rest after one more rejection;
@@ -570,9 +580,12 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
 #pragma unroll
       for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
       if (lane < (int)C) st_peer_f64(mapa(smem_u32(&S.sums[slot][warp][rank]), lane), x);
+    } else if (warp == 2 && lane < (int)C) {
+      st_peer_u32(mapa(smem_u32(&S.steps[slot][rank]), lane), S.step);
     }
     cluster_sync();
     if (warp == 0) {
+      apart = __any_sync(0xffffffffu, lane < (int)C && S.steps[slot][lane] != S.step);
       double t = lane < (int)C ? S.sums[slot][0][lane] : 0.0, z = lane < (int)C ? S.sums[slot][1][lane] : 0.0;
 #pragma unroll
       for (int off = kMaxCluster / 2; off; off >>= 1) {
@@ -607,6 +620,15 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       __syncwarp();
     }
   }
+
+  if (S.op == OP_APART) {  // (nobody waits for this block, nor stores into it, any more)
+    if (rank == 0) {
+      for (int k = tid; k < n; k += kThreads) path[k] = -1;
+      if (tid == 0) P.n_path[b] = 0, P.next_token[b] = -1;
+    }
+    return;
+  }
+  if (warp == 2 && lane < (int)C) st_peer_u32(mapa(smem_u32(&S.steps[turn & 1][rank]), lane), S.step);
 
   // ---- the draw: `piece` and S.sums hold the final P, unscaled, in order ----
   if (tid == 0 && rank == 0) {

@@ -260,6 +260,21 @@ __device__ __forceinline__ double exp2_table(double d, double c, bool low, const
   return low ? 0.0 : e;
 }
 
+template <int N>
+__device__ __forceinline__ double sum_of(const double (&v)[N]) {
+  double w = (v[0] + v[1]) + (v[2] + v[3]);
+  if constexpr (N == 8) w += (v[4] + v[5]) + (v[6] + v[7]);
+  return w;
+}
+
+// max(v f - q, 0) of a value and the draft's probability.  The product is rounded as q's was, and
+// the sums behind f and q's factor are formed in one order: where target and draft are the same
+// row the rest is exactly 0.  (A NaN stays.)
+__device__ __forceinline__ double rest(double v, double f, double q) {
+  const double x = __dsub_rn(__dmul_rn(v, f), q);
+  return x < 0.0 ? 0.0 : x;
+}
+
 enum Op { OP_DONE, OP_SUMS, OP_REST, OP_AGAIN, OP_APART };
 
 struct Ctl {
@@ -536,8 +551,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
             for (int k = 0; k < kPer; ++k) at_q[k * kThreads] = q[k];
         }
         if (rounds == 0) {
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) sq += q[k];
+          sq += sum_of<kPer>(q);
         } else {
 #pragma unroll
           for (int k = 0; k < kPer; ++k) q[k] *= iQ;
@@ -547,8 +561,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
             const double f = from_kept ? scale : y == 0 ? iP : S.iZ[y - 1];
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-              v[k] = v[k] * f - q[k];
-              if (v[k] < 0.0) v[k] = 0.0;
+              v[k] = rest(v[k], f, q[k]);
             }
           }
         }
@@ -563,15 +576,17 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
             if (at == k) v[k] = 0.0;
         }
       }
-      double w = (v[0] + v[1]) + (v[2] + v[3]);
-      if constexpr (kPer == 8) w += (v[4] + v[5]) + (v[6] + v[7]);
+      double w = sum_of<kPer>(v);
+      sv += w;
 #pragma unroll
       for (int off = 16; off; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
       if (lane == 0) piece[s * kWarps + warp] = w;
-      sv += w;
     }
 #pragma unroll
-    for (int off = 16; off; off >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, off);
+    for (int off = 16; off; off >>= 1) {
+      sv += __shfl_xor_sync(0xffffffffu, sv, off);
+      sq += __shfl_xor_sync(0xffffffffu, sq, off);
+    }
     if (lane == 0) S.warp_sum[0][warp] = sv, S.warp_sum[1][warp] = sq;
     const int slot = turn++ & 1;
     __syncthreads();
@@ -594,8 +609,9 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       }
       if (lane == 0) S.total = t;
       if (op == OP_SUMS) {
-        // what was taken out of P belongs to the sum of its exponentials
+        // what was taken out of P belongs to the sum of its exponentials (and a NaN makes it none)
         for (int k = 0; k < S.n_gone; ++k) t += S.p[S.gone[k]];
+        if (!DRAFT && lane == 0 && isnan(t)) S.total = t;
         const double iP = 1.0 / (lane == 1 ? z : t);
         if (lane == 0) S.iP = iP, S.kept = 0;
         if (lane == 1) S.iQ = iP;
@@ -702,8 +718,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
               const float dl = to_f(dp[j + k]);
               const double q = exp2_table((double)dl - mq, dc, (dl - mdf) * dcf <= -1000.f, S.table) * S.iQ;
               for (int y = 0; y < rounds; ++y) {
-                v[k] = v[k] * (y == 0 ? S.iP : S.iZ[y - 1]) - q;
-                if (v[k] < 0.0) v[k] = 0.0;
+                v[k] = rest(v[k], y == 0 ? S.iP : S.iZ[y - 1], q);
               }
             } else {
               for (int y = 0; y < S.n_gone; ++y)

@@ -203,6 +203,27 @@ def test_rows_that_are_no_distribution_at_temperature_zero(sampled):
     assert nxt.tolist()[:4] == [-1] * 4
 
 
+def test_a_rejected_token_without_a_number_leaves_no_distribution():
+    x = inputs(3, 4, 500, "star", False, seed=9)
+    x["u"][:] = 0.999
+    for b in range(3):
+        x["target"][b, 0, int(x["tokens"][b, 1 + b])] = float("nan")
+    path, n_path, nxt = call(**x)
+    assert n_path.tolist() == [1, 1, 1] and nxt.tolist() == [-1, -1, -1]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [2, 7, 31, 1000, 50257])
+def test_a_draft_that_equals_the_target_leaves_nothing(dtype, V):
+    # tokens outside the vocabulary are rejected; max(P - q, 0) is nothing, to the bit, and P stays
+    x = inputs(12, 4, V, "star", True, dtype, seed=V)
+    x["draft"] = x["target"].clone()
+    x["tokens"][:, 1], x["tokens"][:, 2], x["tokens"][:, 3] = -1, V, V + 5
+    x["temperature"] = torch.linspace(0.5, 1.6, 12)
+    x["draft_temperature"] = x["temperature"].clone()
+    assert check(**x) == [1] * 12
+
+
 def test_odd_strides_and_unaligned_rows():
     x = inputs(2, 5, 1000, "tree", True, torch.bfloat16, seed=7)
     whole = {}

@@ -332,31 +332,36 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   if (tid < kTable * kCopies && !greedy) S.table[tid] = exp2(tid / kCopies / (double)kTable);
   cluster_sync();  // also: every block of the cluster has started
   griddep_wait();  // row_stats is done
-  // a row's statistics from its chunks, a warp per row
+  // a row's statistics from its chunks, half a warp per row (its lanes side by side take 16 chunks)
+  const int n_rows = nn * (sampled ? 2 : 1), in = lane & 15;
 #pragma unroll 1
-  for (int x = warp; x < nn * (sampled ? 2 : 1); x += kWarps) {
+  for (int x = warp * 2 + (lane >> 4); __any_sync(0xffffffffu, x < n_rows); x += kWarps * 2) {
+    const bool there = x < n_rows;
     const int d = x >= nn, i = d ? x - nn : x;
     const Stat* st = P.stats + ((int64_t)(d * P.B + b) * n + i) * P.chunks;
     float m = -INFINITY, z = 0.f;
     int idx = 0x7fffffff;
     const float c = d ? dcf : tcf;
 #pragma unroll 1
-    for (int k = lane; k < P.chunks; k += 32) {
+    for (int k = there ? in : P.chunks; k < P.chunks; k += 16) {
       const Stat s = st[k];
       if (s.m > m) idx = s.idx;  // chunks in order: an equal maximum keeps the lower index
       const float top = fmaxf(m, s.m), base = top == -INFINITY ? 0.f : top;
       z = z * ex2((m - base) * c) + s.s * ex2((s.m - base) * c);
       m = top;
     }
+    __syncwarp();
     float top = m;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    for (int off = 8; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     z *= ex2((m - (top == -INFINITY ? 0.f : top)) * c);
     idx = m == top ? idx : 0x7fffffff;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-    idx = __reduce_min_sync(0xffffffffu, idx);
-    if (lane == 0) {
+    for (int off = 8; off; off >>= 1) {
+      z += __shfl_xor_sync(0xffffffffu, z, off);
+      idx = min(idx, __shfl_xor_sync(0xffffffffu, idx, off));
+    }
+    if (there && in == 0) {
       S.m[d][i] = top, S.z[d][i] = z;
       if (!d) S.idx[i] = z > 0.f && z < INFINITY ? idx : -1;  // (else no distribution)
     }

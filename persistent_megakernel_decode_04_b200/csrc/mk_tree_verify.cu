@@ -16,7 +16,7 @@
 //
 // Bound: the walk's latency.  A pass over a row of 128255 words by 8 blocks takes 6 to 9 us, a third
 // of it exchange and control, the rest fp64 arithmetic at half its rate (16 blocks: 4 to 5).  16
-// sequences x 9 nodes of that size (bf16, sampled drafts) take 67 us, of which row_stats 15 and the
+// sequences x 9 nodes of that size (bf16, sampled drafts) take 66 us, of which row_stats 15 and the
 // longest walk nearly all the rest; one chain of 5 (fp32, 128256 words) 17 us; 4 x 26 nodes of 65536
 // words without a draft 20 us.
 //

@@ -99,8 +99,10 @@ struct Ctl {
   uint32_t tmem, abort;
   uint32_t bad_v;  // infinite or NaN values among the drafts that this block saw
   // Counters that only grow, for roles that may be more than one step apart (an mbarrier's parity
-  // cannot tell two steps from none): V tiles to clean that were issued; helpers' shares done.
-  uint32_t v_issued, v_clean;
+  // cannot tell two steps from none): V tiles to clean that were issued; each helper's shares done.
+  // (One count of both helpers' shares would not do: they do not wait for each other, so two shares
+  // may be one helper's of two tiles.)
+  uint32_t v_issued, v_clean[2];
   uint32_t bad_any;  // some block of the cluster has bad_v set
   // (maximum, sum) of every row that this block finishes from every block of the cluster
   float2 stat[kRows + kMaxCluster];
@@ -149,6 +151,13 @@ __device__ __forceinline__ bool wait_count(const uint32_t* at, uint32_t value, c
 }
 __device__ __forceinline__ bool wait_count_warp(const uint32_t* at, uint32_t value, const Params& P, Ctl& S) {
   return __all_sync(0xffffffffu, wait_count(at, value, P, S));
+}
+// Whether the helpers found infinite or NaN values among the drafts of this block's tiles, all of
+// which they have cleaned by now (their counts make what they stored before visible).
+__device__ __forceinline__ bool found_bad_v(const Ctl& S) {
+  ld_acquire_cta_shared(&S.v_clean[0]);
+  ld_acquire_cta_shared(&S.v_clean[1]);
+  return S.bad_v != 0;
 }
 __device__ __forceinline__ void count_up(uint32_t* at) {
   asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(at)) : "memory");
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&S.q_full, kSoft);
       mbar_init(&S.mma_done, 1);
       mbar_init(&S.anc_full, 1);
-      S.abort = S.bad_v = S.bad_any = S.v_issued = S.v_clean = 0;
+      S.abort = S.bad_v = S.bad_any = S.v_issued = S.v_clean[0] = S.v_clean[1] = 0;
       fence_mbar_init();
     }
   } else if (warp == kMmaWarp) {
@@ -555,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (j >= 0) {
           const int x = v_index(j, T), stage = x % Ge::kStages;
           ok = wait_warp(&S.full[stage], (x / Ge::kStages) & 1, P, S) &&
-               (j < edge || wait_count_warp(&S.v_clean, 2 * (j - edge + 1), P, S)) &&
+               (j < edge || (wait_count_warp(&S.v_clean[0], j - edge + 1, P, S) &&
+                             wait_count_warp(&S.v_clean[1], j - edge + 1, P, S))) &&
                wait_warp(&S.p_full[buf], (j >> 1) & 1, P, S);
           if (!ok) break;
           tc_fence_after();
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) count_up(&S.v_clean);
+      if (lane == 0) count_up(&S.v_clean[warp - kHelper]);
     }
   } else {
     // ---- softmax: one thread per row ----
@@ -779,13 +789,13 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
         }
-        if (S.bad_v && real) add_nonfinite<FP16, WIDE>(P, S, b, h, len, node, 0, D, out);
+        if (real && found_bad_v(S)) add_nonfinite<FP16, WIDE>(P, S, b, h, len, node, 0, D, out);
       } else {
         // a row's statistics and O to the block that finishes it, over that block's Q and ring
         const int owner = real ? row / per : 0, x = row - owner * per;
         if (real) {
           st_peer_f2(mapa(smem_u32(&S.stat[x * C + rank]), owner), m, l);
-          if (S.bad_v) st_peer_u32(mapa(smem_u32(&S.bad_any), owner), 1);
+          if (found_bad_v(S)) st_peer_u32(mapa(smem_u32(&S.bad_any), owner), 1);
         }
         if (T > 0) {
           // 32 columns at a time through a corner of shared memory, so that a row's 128 bytes leave

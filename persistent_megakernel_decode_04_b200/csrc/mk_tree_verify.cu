@@ -275,7 +275,7 @@ __device__ __forceinline__ double rest(double v, double f, double q) {
   return x < 0.0 ? 0.0 : x;
 }
 
-enum Op { OP_DONE, OP_SUMS, OP_REST, OP_AGAIN, OP_APART };
+enum Op { OP_DONE, OP_SUMS, OP_LAST, OP_REST, OP_AGAIN, OP_APART };
 
 struct Ctl {
   double table[kTable * kCopies];
@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   if (tid < kTable * kCopies && !greedy) S.table[tid] = exp2(tid / kCopies / (double)kTable);
   cluster_sync();  // also: every block of the cluster has started
   griddep_wait();  // row_stats is done
-  // a row's statistics from its chunks, half a warp per row (its lanes side by side take 16 chunks)
+  // a row's statistics from its chunks, half a warp per row (its lanes side by side take 16 chunks);
+  // for the draft's rows of nodes without children, which row_stats leaves out, they mean nothing and are not used
   const int n_rows = nn * (sampled ? 2 : 1), in = lane & 15;
 #pragma unroll 1
   for (int x = warp * 2 + (lane >> 4); __any_sync(0xffffffffu, x < n_rows); x += kWarps * 2) {
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         }
         ++c;
       }
-      if (op == OP_DONE && !greedy && nn > 0 && !summed) op = rounds > 0 ? OP_AGAIN : OP_SUMS;
+      if (op == OP_DONE && !greedy && nn > 0 && !summed) op = rounds > 0 ? OP_AGAIN : OP_LAST;
       if (apart) op = OP_APART;
       __syncwarp();
       if (lane == 0) {
@@ -490,18 +491,21 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
     if (op == OP_DONE || op == OP_APART) break;
     // ---- a pass over the current node's rows: this block's slice, kPer elements per thread and step.
     // OP_SUMS: sums of the exponentials (without the tokens that are gone: also what is drawn
-    // from when nothing was rejected).  OP_REST: the sum of the rest after one more rejection;
-    // OP_AGAIN: after the rejections so far (the last OP_REST left nothing, and P stayed).
+    // from when nothing was rejected).  OP_LAST: the same for the draw alone, with no child left to
+    // ask; it reads no draft row (a node without children need not have one).  OP_REST: the sum of the
+    // rest after one more rejection; OP_AGAIN: after the rejections so far (the last OP_REST left
+    // nothing, and P stayed).
     const int node = S.cur;
     const T* tp = target + node * P.t_node;
-    const T* dp = draft + (sampled ? node * P.d_node : 0);
+    const bool with_q = sampled && op != OP_LAST;
+    const T* dp = draft + (with_q ? node * P.d_node : 0);
     // slices and steps are counted from the last 4-element border before the target's row
     const int lead = (int)((reinterpret_cast<uintptr_t>(tp) / sizeof(T)) & 3);
     const bool d_vec = ((reinterpret_cast<uintptr_t>(dp) / sizeof(T)) & 3) == (uintptr_t)lead;
     const int lo = (int)rank * slice - lead, hi = min(V, lo + slice);
     const float mtf = S.m[0][node], mdf = S.m[1][node];
     const double mp = mtf, mq = mdf;
-    const int rounds = op == OP_SUMS ? 0 : S.rounds + (op == OP_REST), n_gone = S.n_gone;
+    const int rounds = op == OP_SUMS || op == OP_LAST ? 0 : S.rounds + (op == OP_REST), n_gone = S.n_gone;
     const double iP = S.iP, iQ = S.iQ;
     auto load4 = [&](const T* row, bool vec, int j, float* x) {
       if (vec && j >= 0 && j + 4 <= hi) {
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
       if (!from_kept)
 #pragma unroll
         for (int k = 0; k < kPer; k += 4) load4(tp, true, j + k, tl + k);
-      if (sampled && !q_from_kept)
+      if (with_q && !q_from_kept)
 #pragma unroll
         for (int k = 0; k < kPer; k += 4) load4(dp, d_vec, j + k, dl + k);
       if (from_kept) {
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] = exp2_table((double)tl[k] - mp, tc, (tl[k] - mtf) * tcf <= -1000.f, S.table);
       }
-      if (sampled) {
+      if (with_q) {
         if (q_from_kept) {
 #pragma unroll
           for (int k = 0; k < kPer; ++k) q[k] = at_q[k * kThreads];
@@ -570,6 +574,8 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
             }
           }
         }
+      }
+      if (sampled) {
         if (store)
 #pragma unroll
           for (int k = 0; k < kPer; ++k) at_v[k * kThreads] = v[k];
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
         z += __shfl_xor_sync(0xffffffffu, z, off);
       }
       if (lane == 0) S.total = t;
-      if (op == OP_SUMS) {
+      if (op == OP_SUMS || op == OP_LAST) {
         // what was taken out of P belongs to the sum of its exponentials (and a NaN makes it none)
         for (int k = 0; k < S.n_gone; ++k) t += S.p[S.gone[k]];
         if (!DRAFT && lane == 0 && isnan(t)) S.total = t;

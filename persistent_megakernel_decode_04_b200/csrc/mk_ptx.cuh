@@ -312,6 +312,21 @@ __device__ __forceinline__ uint64_t tc_smem_desc(uint32_t saddr, uint32_t lbo, u
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Cluster barrier, for all threads of a cluster's blocks.  The aligned forms want a warp's lanes
+// together, and callers come from code that lanes take apart.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+
 // A kernel launched early may start before the one ahead of it in the stream has ended: until this
 // returns it reads and writes no memory that others use.  Every block waits (then the kernel after
 // it, which waits for this one, follows all that ran before).

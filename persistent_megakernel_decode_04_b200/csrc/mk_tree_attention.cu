@@ -293,8 +293,6 @@ __device__ __forceinline__ void st_peer_v4(uint32_t addr, const uint4& x) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
@@ -663,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.q_full);
+    __syncwarp();  // here and below: the warp-wide tcgen05 forms want the lanes together
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_base, o_at = lane_base + 128;
     const int node = first + local;
@@ -753,15 +752,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[j & 1]);
+      __syncwarp();
     }
     // ---- the end: every product is done, Q and the ring are read out ----
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel may take the places that fall free
     if (T > 0) ok = ok && wait_warp(&S.o_full, 0, P, S);
     tc_fence_after();
-    if (C > 1) {  // every block's Q and ring are read out
-      cluster_arrive();
-      cluster_wait();
-    }
+    if (C > 1) cluster_sync();  // every block's Q and ring are read out
     if (any) {
       if (C == 1) {
         if (ok) ok = wait_warp(&S.anc_full, 0, P, S);
@@ -788,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     pack16<FP16>(f[0], f[1]), pack16<FP16>(f[2], f[3]), pack16<FP16>(f[4], f[5]), pack16<FP16>(f[6], f[7]));
               }
             }
+          __syncwarp();
         }
         if (real && found_bad_v(S)) add_nonfinite<FP16, WIDE>(P, S, b, h, len, node, 0, D, out);
       } else {
@@ -797,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           st_peer_f2(mapa(smem_u32(&S.stat[x * C + rank]), owner), m, l);
           if (found_bad_v(S)) st_peer_u32(mapa(smem_u32(&S.bad_any), owner), 1);
         }
+        __syncwarp();
         if (T > 0) {
           // 32 columns at a time through a corner of shared memory, so that a row's 128 bytes leave
           // together: eight lanes per row
@@ -829,12 +828,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncwarp();
   if (C > 1) {
-    if (warp >= kSoft) {
-      cluster_arrive();
-      cluster_wait();
-    }
-    cluster_arrive();  // every partial result has arrived; no block touches another's memory after this
-    cluster_wait();
+    if (warp >= kSoft) cluster_sync();
+    cluster_sync();  // every partial result has arrived; no block touches another's memory after this
   } else {
     __syncthreads();
   }

@@ -235,10 +235,6 @@ __device__ __forceinline__ void st_peer_f64(uint32_t addr, double x) {
 __device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t x) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // 2^y, y = d c, for -1000 <= y <= 0 by a table of 2^(k / 16) and the series of 2^r in the remainder (|r| <=
 // 1/32; the term behind the fifth is below 1.5e-13).  The method is P. T. P. Tang's, "Table-driven

@@ -389,7 +389,8 @@ def mk_attention_debug_drop_unit(unit: int):
 
 
 # ---- speculative decoding: these take torch tensors and read sizes, strides and types off them.
-# A decoding loop makes these calls for kernels of a few microseconds, so the checks are kept
+# Like torch's own operators they run on the current stream of the tensors' device unless they are
+# given one (0: the NULL stream).  A decoding loop makes these calls for kernels of a few microseconds, so the checks are kept
 # cheap: plain comparisons, and the shape structs packed instead of built field by field.
 
 _TREE_SHAPE = struct.Struct("8i12q")
@@ -421,19 +422,21 @@ def _index(t, shape, dtype, what):
     return t.data_ptr()
 
 
-def _call(torch, f, tensors, *args):
-    """f(*args) with the tensors' device current; they all have to be on it."""
+def _call(torch, f, tensors, stream, *args):
+    """f(*args, stream) with the tensors' device current; they all have to be on it.  Without a
+    stream: the device's current one."""
     dev = tensors[0].get_device()
     if dev < 0:
         _refuse("tensors must be on a CUDA device")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             _refuse(f"tensors on {tensors[0].device} and {t.device}")
+    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
     if _devices == 1 or torch.cuda.current_device() == dev:
-        rc = f(*args)
+        rc = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            rc = f(*args)
+            rc = f(*args, stream)
     if rc:
         _check(rc)
 
@@ -462,20 +465,22 @@ def mk_tree_attention(q, k, v, o, parents, n_nodes, lens, scale: float, stream=N
     if not q3 == k3 == v3 == o3 == 1:
         _refuse("the last axis of q, k, v and o must be contiguous")
     i32 = torch.int32
-    _call(torch, _lib.mk_tree_attention, (q, k, v, o, parents, lens, n_nodes),
+    _call(torch, _lib.mk_tree_attention, (q, k, v, o, parents, lens, n_nodes), stream,
           _TREE_SHAPE.pack(code, wide, B, n, hq, hkv, d, S, q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2),
           q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _index(parents, (B, n), i32, "parents"),
-          _index(n_nodes, (B,), i32, "n_nodes"), _index(lens, (B,), i32, "lens"), scale, _stream(stream))
+          _index(n_nodes, (B,), i32, "n_nodes"), _index(lens, (B,), i32, "lens"), scale)
 
 
 def mk_tree_attention_status(stream=None) -> int:
     """MK_OK, or MK_ERR_DEVICE_TIMEOUT if a tree attention since the last status call had a device
-    wait run out (returned, not raised)."""
-    return _lib.mk_tree_attention_status(_stream(stream))
+    wait run out (returned, not raised).  Waits for the stream (None: the current one)."""
+    torch, _ = _types or _torch_types()
+    return _lib.mk_tree_attention_status(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
 
 
 def mk_tree_forward(ctx, tokens, parents, n_nodes, lens, B: int, n: int, kv_cache, logits, stream=None):
-    """The target model's logits after every node of B drafted trees; see include/mk.h."""
+    """The target model's logits after every node of B drafted trees; see include/mk.h.  (As with the
+    context's other calls, no stream is the NULL stream.)"""
     _check(_lib.mk_tree_forward(ctx, _ptr(tokens), _ptr(parents), _ptr(n_nodes), _ptr(lens), int(B), int(n),
                                 _ptr(kv_cache), _ptr(logits), _stream(stream)), ctx)
 
@@ -504,14 +509,13 @@ def mk_tree_verify(target, draft, tokens, parents, n_nodes, u, r, temperature, d
     i32, f32, one, two = torch.int32, torch.float32, (B,), (B, n)
     _call(torch, _lib.mk_tree_verify,
           (target, tokens, parents, u, r, path, n_path, next_token, workspace, draft, n_nodes, temperature,
-           draft_temperature),
+           draft_temperature), stream,
           _VERIFY_SHAPE.pack(code, B, n, V, t0, t1, d0, d1), target.data_ptr(),
           None if draft is None else draft.data_ptr(), _index(tokens, two, i32, "tokens"),
           _index(parents, two, i32, "parents"), _index(n_nodes, one, i32, "n_nodes"), _index(u, two, f32, "u"),
           _index(r, one, f32, "r"), _index(temperature, one, f32, "temperature"),
           _index(draft_temperature, one, f32, "draft_temperature"), _index(path, two, i32, "path"),
-          _index(n_path, one, i32, "n_path"), _index(next_token, one, i32, "next_token"), workspace.data_ptr(),
-          _stream(stream))
+          _index(n_path, one, i32, "n_path"), _index(next_token, one, i32, "next_token"), workspace.data_ptr())
 
 
 def _cache(kv, B):
@@ -528,9 +532,9 @@ def mk_cache_commit(kv, path, n_path, lens, new_lens, stream=None):
     path[b][j] moves to lens[b] + j.  path [B, n], n_path, lens, new_lens [B] int32."""
     torch, _ = _types or _torch_types()
     B, n, i32 = lens.shape[0], path.shape[-1], torch.int32
-    _call(torch, _lib.mk_cache_commit, (kv, path, n_path, lens, new_lens), _cache(kv, B), kv.data_ptr(),
-          _index(path, (B, n), i32, "path"), n, _index(n_path, (B,), i32, "n_path"), _index(lens, (B,), i32, "lens"),
-          _index(new_lens, (B,), i32, "new_lens"), _stream(stream))
+    _call(torch, _lib.mk_cache_commit, (kv, path, n_path, lens, new_lens), stream, _cache(kv, B),
+          kv.data_ptr(), _index(path, (B, n), i32, "path"), n, _index(n_path, (B,), i32, "n_path"),
+          _index(lens, (B,), i32, "lens"), _index(new_lens, (B,), i32, "new_lens"))
 
 
 def mk_cache_reorder(kv, src, lens, new_lens, stream=None):
@@ -538,9 +542,8 @@ def mk_cache_reorder(kv, src, lens, new_lens, stream=None):
     lens, new_lens [B] int32."""
     torch, _ = _types or _torch_types()
     B, i32 = lens.shape[0], torch.int32
-    _call(torch, _lib.mk_cache_reorder, (kv, src, lens, new_lens), _cache(kv, B), kv.data_ptr(),
-          _index(src, (B,), i32, "src"), _index(lens, (B,), i32, "lens"), _index(new_lens, (B,), i32, "new_lens"),
-          _stream(stream))
+    _call(torch, _lib.mk_cache_reorder, (kv, src, lens, new_lens), stream, _cache(kv, B), kv.data_ptr(),
+          _index(src, (B,), i32, "src"), _index(lens, (B,), i32, "lens"), _index(new_lens, (B,), i32, "new_lens"))
 
 
 def mk_last_error(ctx=None) -> str:
@@ -659,14 +662,14 @@ class Megakernel:
         forwarded; returns the new lengths (int32 CUDA [B])."""
         import torch
         new_lens = torch.empty_like(lens)
-        mk_cache_commit(self.kv_view(), path, n_path, lens, new_lens, self.stream)
+        mk_cache_commit(self.kv_view(), path, n_path, lens, new_lens, self.stream or 0)
         return new_lens
 
     def reorder(self, src, lens):
         """Sequence b takes over sequence src[b]'s cache rows; returns the new lengths."""
         import torch
         new_lens = torch.empty_like(lens)
-        mk_cache_reorder(self.kv_view(), src, lens, new_lens, self.stream)
+        mk_cache_reorder(self.kv_view(), src, lens, new_lens, self.stream or 0)
         return new_lens
 
     def calibrate(self, tokens, steps: int = 2, rounds: int = 3):

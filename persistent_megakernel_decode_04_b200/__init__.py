@@ -653,6 +653,8 @@ class Megakernel:
         for t, shape, what in ((tokens, (B, n), "tokens"), (parents, (B, n), "parents"), (lens, (B,), "lens"),
                                (n_nodes, (B,), "n_nodes")):
             _index(t, shape, i32, what)
+            if t is not None and t.get_device() != self.device:
+                _refuse(f"{what} must be on cuda:{self.device}, the model's device")
         out = torch.empty((B, n, self.cfg.vocab), dtype=torch.float32, device=tokens.device)
         mk_tree_forward(self.ctx, tokens, parents, n_nodes, lens, B, n, self.kv, out, self.stream)
         return out

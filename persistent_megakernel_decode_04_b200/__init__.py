@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+from contextlib import contextmanager
 from dataclasses import dataclass
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -643,10 +644,27 @@ class Megakernel:
         mk_decode_steps(self.ctx, tokens, n_steps, self.kv, self.logits, out, self.stream)
         return self.logits[:B], out[:, :B]
 
+    @contextmanager
+    def _joined(self):
+        """For calls on the context's stream with tensors of the caller's: where torch's current
+        stream is another one, the context's stream waits for it first and it waits for the calls, so
+        that inputs are there, results can be used at once and the memory of neither is reused early."""
+        import torch
+        with torch.cuda.device(self.device):
+            here, mine = torch.cuda.current_stream(), _stream(self.stream) or 0
+            if here.cuda_stream == mine:
+                yield mine
+                return
+            s = torch.cuda.ExternalStream(mine) if mine else torch.cuda.default_stream()
+            s.wait_stream(here)
+            yield mine
+            here.wait_stream(s)
+
     def tree_forward(self, tokens, parents, lens, n_nodes=None):
         """Logits [B, n, vocab] after every node of drafted trees (tokens, parents: int32 CUDA [B, n];
         lens: int32 CUDA [B], the rows of each sequence in the cache, all of them known to the
-        device: the positions kept by the context are not used).  Node 0 is the last token."""
+        device: the positions kept by the context are not used).  Node 0 is the last token.  This,
+        commit and reorder run on the context's stream, in order with the current one."""
         import torch
         B, n = tokens.shape
         i32 = torch.int32
@@ -656,7 +674,8 @@ class Megakernel:
             if t is not None and t.get_device() != self.device:
                 _refuse(f"{what} must be on cuda:{self.device}, the model's device")
         out = torch.empty((B, n, self.cfg.vocab), dtype=torch.float32, device=tokens.device)
-        mk_tree_forward(self.ctx, tokens, parents, n_nodes, lens, B, n, self.kv, out, self.stream)
+        with self._joined() as stream:
+            mk_tree_forward(self.ctx, tokens, parents, n_nodes, lens, B, n, self.kv, out, stream)
         return out
 
     def commit(self, path, n_path, lens):
@@ -664,14 +683,16 @@ class Megakernel:
         forwarded; returns the new lengths (int32 CUDA [B])."""
         import torch
         new_lens = torch.empty_like(lens)
-        mk_cache_commit(self.kv_view(), path, n_path, lens, new_lens, self.stream or 0)
+        with self._joined() as stream:
+            mk_cache_commit(self.kv_view(), path, n_path, lens, new_lens, stream)
         return new_lens
 
     def reorder(self, src, lens):
         """Sequence b takes over sequence src[b]'s cache rows; returns the new lengths."""
         import torch
         new_lens = torch.empty_like(lens)
-        mk_cache_reorder(self.kv_view(), src, lens, new_lens, self.stream or 0)
+        with self._joined() as stream:
+            mk_cache_reorder(self.kv_view(), src, lens, new_lens, stream)
         return new_lens
 
     def calibrate(self, tokens, steps: int = 2, rounds: int = 3):

@@ -640,9 +640,21 @@ class Megakernel:
         returns (logits of the last step [B, vocab], picked tokens [n_steps, B])."""
         import torch
         B = tokens.shape[0]
-        out = torch.empty((n_steps, self.cfg.max_batch), dtype=torch.int32, device=tokens.device)
+        mine = self._other_stream()
+        with torch.cuda.stream(mine):  # memory of the stream that writes it: nothing else is queued on it
+            out = torch.empty((n_steps, self.cfg.max_batch), dtype=torch.int32, device=tokens.device)
+        if mine is not None:
+            out.record_stream(torch.cuda.current_stream(self.device))  # given back behind what the caller reads it with
         mk_decode_steps(self.ctx, tokens, n_steps, self.kv, self.logits, out, self.stream)
         return self.logits[:B], out[:, :B]
+
+    def _other_stream(self):
+        """The context's stream as a torch stream, or None where it is torch's current one."""
+        import torch
+        handle = _stream(self.stream) or 0
+        if handle == torch._C._cuda_getCurrentRawStream(self.device):
+            return None
+        return torch.cuda.ExternalStream(handle, self.device) if handle else torch.cuda.default_stream(self.device)
 
     @contextmanager
     def _joined(self):
@@ -651,14 +663,14 @@ class Megakernel:
         that inputs are there, results can be used at once and the memory of neither is reused early."""
         import torch
         with torch.cuda.device(self.device):
-            here, mine = torch.cuda.current_stream(), _stream(self.stream) or 0
-            if here.cuda_stream == mine:
-                yield mine
+            mine = self._other_stream()
+            if mine is None:
+                yield self.stream or 0
                 return
-            s = torch.cuda.ExternalStream(mine) if mine else torch.cuda.default_stream()
-            s.wait_stream(here)
+            here = torch.cuda.current_stream()
+            mine.wait_stream(here)
             yield mine
-            here.wait_stream(s)
+            here.wait_stream(mine)
 
     def tree_forward(self, tokens, parents, lens, n_nodes=None):
         """Logits [B, n, vocab] after every node of drafted trees (tokens, parents: int32 CUDA [B, n];

@@ -77,3 +77,25 @@ def test_speculative_calls_are_in_order_with_the_current_stream(own, current, ha
     torch.cuda.synchronize()
     assert m.sync_status() == mk.MK_OK and mk.mk_tree_attention_status() == mk.MK_OK
     m.close()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_decode_steps_writes_no_memory_that_the_current_stream_still_uses(handle):
+    s, here, n = torch.cuda.Stream(), torch.cuda.Stream(), 3
+    want = None
+    for stream in (None, s.cuda_stream if handle else s):
+        m = model(stream)
+        m.set_positions([20, 20])
+        tokens = i32([3, 500])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(here):
+            torch.cuda._sleep(LATE)
+            x = torch.empty((n, 2), dtype=torch.int32, device=DEV)
+            x.fill_(-7)  # when the steps are long done
+            del x
+            picks = m.decode_steps(tokens, n)[1]
+        assert m.sync_status() == mk.MK_OK
+        torch.cuda.synchronize()
+        want = picks.clone() if want is None else want
+        assert (picks >= 0).all() and torch.equal(picks, want)
+        m.close()

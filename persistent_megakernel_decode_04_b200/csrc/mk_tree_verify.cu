@@ -22,9 +22,13 @@
 //
 // Precision.  A draw from 1e5 words by cumulative sums meets a border within 1e-7 in about every
 // hundredth draw, so sums that decide a draw are formed in fp64 from exponentials good to 1e-13.
-// Acceptance compares two numbers: fp32 statistics (relative error below 4e-6: 2^-22 for each
-// of at most five exponentials in a row, 2^-24 for each of at most 40 additions in a row) decide
-// unless the two are that close; then the row's sums are formed in fp64 first.
+// Acceptance compares two numbers, each with one row's fp32 sum in it: those decide unless the two
+// are within kClose; then the rows' sums are formed in fp64 first.  A sum is off by less than 9e-6
+// relative: 2^-22 for each of at most 13 exponentials in a row (a value's own and what takes it to
+// higher maxima) and 2^-24 for the product with each, 2^-24 for each of at most 40 additions in a row,
+// and 2.5e-6 from the exponents: the difference, the product and log2(e) / temperature are rounded
+// four times, which moves a value by 4 x 2^-24 ln 2 of its exponent, whose mean over the sum's weights is
+// at most 15.2 (2^20 words).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -46,7 +50,7 @@ constexpr int kChunk = 8192;        // elements of a row per block of row_stats
 constexpr int kThreads = 512;       // walk
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr float kClose = 1e-5f;
+constexpr float kClose = 2e-5f;     // two sums' errors
 // elements per thread and step of a pass: eight keep more exponentials in flight; without a draft
 // four need few enough registers for row_stats's blocks beside the walk's
 template <bool DRAFT>

@@ -401,9 +401,12 @@ __device__ __forceinline__ void merge(const Params& P, const Ctl& S, const float
     float sum = st.y * f;
     for (int off = C / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const int local = (int)(r * P.inv_g >> 16), g = r - local * P.G, node = first + local;
-    f = sum == 0.f || !alive(S, node) ? 0.f : __fdividef(f, sum);
+    // (a node that sees rows and has no weight for any has scores of -infinity only: 0 / 0)
+    const bool live = alive(S, node);
+    const float none = live && sum == 0.f ? __int_as_float(0x7fffffff) : 0.f;
+    f = sum == 0.f || !live ? 0.f : __fdividef(f, sum);
     const float* src = parts + (r - r0) * Ge::kOStride + col;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc[4] = {none, none, none, none};
 #pragma unroll 4
     for (int p = 0; p < C; ++p) {
       const float fp = __shfl_sync(0xffffffffu, f, p, kLanes);
@@ -762,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (any) {
       if (C == 1) {
         if (ok) ok = wait_warp(&S.anc_full, 0, P, S);
-        const float inv = l == 0.f || !real || !alive(S, node) ? 0.f : 1.f / l;
+        const float inv = !real || !alive(S, node) ? 0.f : 1.f / l;  // (l = 0, scores of -infinity only: 0 x inf, NaN)
         Out<WIDE>* out = static_cast<Out<WIDE>*>(P.o) + (int64_t)b * P.o_seq + (int64_t)node * P.o_node +
                          (int64_t)(h * P.G + row - local * P.G) * P.o_head;
 #pragma unroll 1

@@ -68,3 +68,28 @@ def test_in_every_tile_and_every_group_of_keys(d, dtype, wide, B, n, hq, hkv, le
         g, w = got[seen].float(), value[seen]
         assert torch.equal(g.isnan(), w.isnan()) and torch.equal(g.nan_to_num(0, 1, -1), w.nan_to_num(0, 1, -1))
     assert mk.mk_tree_attention_status() == mk.MK_OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("B,S", [(1, 640), (2, 4096), (300, 200)])  # clusters of several sizes, single blocks
+def test_scores_of_minus_infinity(B, S, d, dtype):
+    """A key of -infinity has no weight; a node that sees no others is 0 / 0."""
+    n, hq, hkv, ln = 4, 4, 2, 150
+    q, k, v = make(B, n, hq, hkv, d, S, dtype, seed=d)
+    q[..., 0] = 1.0
+    k[:, 0, :ln + 1, 0] = float("-inf")  # of the first KV head: all cached rows and node 0
+    parents = torch.tensor([[-1, 0, 1, 0]] * B, dtype=torch.int32, device=DEV)
+    parents[:, 3] = 7                    # not a tree's
+    lens = torch.full((B,), ln, dtype=torch.int32, device=DEV)
+    got = attend(q, k, v, parents, lens)
+    assert mk.mk_tree_attention_status() == mk.MK_OK
+    assert got[:, 0, :2].isnan().all()
+    assert torch.equal(got[:, 1, :2], v[:, 0, ln + 1][:, None].expand(B, 2, d))  # itself alone
+    two = k[:, 0, ln + 1:ln + 3].double()
+    p = torch.softmax(torch.einsum("bhd,brd->bhr", q[:, 2, :2].double(), two) * 0.125, -1)
+    want = torch.einsum("bhr,brd->bhd", p, v[:, 0, ln + 1:ln + 3].double())
+    # output and weights rounded to half an eps each, of |v| below 8; fp32 steps below 2^-12
+    assert ((got[:, 2, :2].double() - want).abs() <= 8 * (torch.finfo(dtype).eps + 2.0 ** -12)).all()
+    assert (got[:, 3] == 0).all()
+    assert got[:, :3, 2:].isfinite().all()

@@ -1,7 +1,7 @@
 // mk_ptx.cuh -- thin inline-PTX wrappers for sm_100a used by the library's kernels:
 // shared-memory mbarriers, bulk and tensor TMA copies, gpu-scope acquire/release and
-// the global timer.  Each wrapper is one PTX instruction (ISA 8.x forms).  At the end, launches whose
-// start overlaps the end of the kernel before.
+// the global timer.  Each wrapper is one PTX instruction (ISA 8.x forms; the cluster barrier has the
+// warp's with it).  At the end, launches whose start overlaps the end of the kernel before.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -311,6 +311,33 @@ __device__ __forceinline__ uint64_t tc_smem_desc(uint32_t saddr, uint32_t lbo, u
 
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Blocks of this block's cluster, its place among them; the address of a peer block's shared memory, and a
+// store there.
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
 
 // Cluster barrier, for all threads of a cluster's blocks.  The aligned forms want a warp's lanes
 // together, and callers come from code that lanes take apart.

@@ -84,7 +84,7 @@ struct Params {
   void* o;
   const int32_t *parents, *n_nodes, *lens;
   int64_t q_seq, q_node, q_head, o_seq, o_node, o_head, v_seq, v_head, v_row;
-  int n, hq, hkv, G, max_seq;
+  int n, hkv, G, max_seq;
   int nt;        // nodes per row tile
   int units;     // row tiles per (sequence, KV head)
   uint32_t inv_g;  // r / G = r * inv_g >> 16 for r < 256
@@ -226,26 +226,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       MK_I8(r, 24), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-      "%14, %15};" ::MK_I8(r, 0), MK_I8(r, 8), "r"(taddr)
-      : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t* r) {
-  if constexpr (N == 16)
-    tmem_st16(taddr, r);
-  else
-    tmem_st32(taddr, r);
-}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -277,31 +258,13 @@ __device__ __forceinline__ void split16(float x, float y, uint32_t& hi, uint32_t
   lo = pack16<FP16>(x - value16<FP16>((uint16_t)hi), y - value16<FP16>((uint16_t)(hi >> 16)));
 }
 
-// Address of a peer block's shared memory, and stores there.
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t x) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
+// Stores to a peer block's shared memory.
 __device__ __forceinline__ void st_peer_f2(uint32_t addr, float x, float y) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 __device__ __forceinline__ void st_peer_v4(uint32_t addr, const uint4& x) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
 }
 
 // Bits rel0 .. rel0 + 31 of what a node sees: every row before its drafts (rel < 0), then its
@@ -946,7 +909,7 @@ int tree_attention(const mk_tree_shape& s, const void* q, const void* k, const v
   P.q_seq = s.q_seq, P.q_node = s.q_node, P.q_head = s.q_head;
   P.o_seq = s.o_seq, P.o_node = s.o_node, P.o_head = s.o_head;
   P.v_seq = s.v_seq, P.v_head = s.v_head, P.v_row = s.v_row;
-  P.n = s.n, P.hq = s.n_q_heads, P.hkv = s.n_kv_heads, P.G = s.n_q_heads / s.n_kv_heads, P.max_seq = s.max_seq;
+  P.n = s.n, P.hkv = s.n_kv_heads, P.G = s.n_q_heads / s.n_kv_heads, P.max_seq = s.max_seq;
   P.nt = kRows / P.G;
   P.inv_g = 65536u / P.G + 1;
   P.c = fabsf(scale) * 1.44269504088896340736f;

@@ -79,12 +79,6 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // -infinity; the largest of a 16-byte piece (NaN left out); its values.
 template <typename T>
 __device__ __forceinline__ T lowest();
@@ -228,16 +222,8 @@ __global__ void __launch_bounds__(kStatThreads) row_stats(const Params P) {
 }
 
 // ---- walk ----
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ void st_peer_f64(uint32_t addr, double x) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(x) : "memory");
-}
-__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t x) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 
 // 2^y, y = d c, for -1000 <= y <= 0 by a table of 2^(k / 16) and the series of 2^r in the remainder (|r| <=
@@ -306,9 +292,7 @@ __global__ void __launch_bounds__(kThreads) walk(const Params P) {
   // (s kPer + k) kThreads + t), the draft's exponentials alike, and sums of 32 kPer elements each
   extern __shared__ double dyn[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t C, rank;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const uint32_t C = cluster_size(), rank = cluster_rank();
   const int b = blockIdx.x / C, n = P.n, V = P.V, nn = in_use(P, b);
   const float temp = P.temperature ? P.temperature[b] : 1.f;
   const bool greedy = temp == 0.f, sampled = DRAFT && !greedy;

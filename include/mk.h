@@ -398,10 +398,11 @@ typedef struct mk_tree_shape {
  *   j in {0 .. lens[b] - 1} and lens[b] + a for a = i, parents[b][i], its parent, ..
  * with G = n_q_heads / n_kv_heads.  n = 1 is decode attention over lens[b] + 1 rows.  Softmax and
  * sums in fp32; the softmax weights are rounded to the inputs' type for the product with v (wide: as
- * the sum of two such values; fp32 q for an fp16 cache is within fp16's range).  k and v: one layer
- * of the decoder's cache, or any such arrays; o overlaps none of the inputs.  Rows that a node does
- * not see have no influence on it, whatever they hold; infinities and NaN in rows that it sees reach
- * its output.
+ * the sum of two such values; fp32 q is within the cache type's range).  k and v: one layer of the
+ * decoder's cache, or any such arrays; o overlaps none of the inputs.  Rows that a node does not see
+ * have no influence on it, whatever they hold; infinities and NaN in rows that it sees reach its output
+ * (an infinity as itself or, where a weight or a part of q rounds to 0, as NaN; a node whose scores are
+ * all -infinity gets NaN).
  * A node whose parents are not a tree's (parents[b][i] outside [-1, i), or such an ancestor) gets
  * zeros.  Requirements: head_dim 64 or 128; n_q_heads % n_kv_heads == 0, G <= 128; 1 <= n <=
  * MK_MAX_TREE_NODES; q, k, v and o 16-byte aligned; scale finite and not 0.  No workspace; calls
@@ -416,7 +417,8 @@ int mk_tree_attention(const mk_tree_shape* shape, const void* q, const void* k, 
 int mk_tree_attention_status(void* stream);
 
 /* The target model's logits after every node, on the prompt kernels with mk_tree_attention (wide) in
- * each layer: as exact as mk_prefill.  tokens: device int32 [B][n];
+ * each layer: as exact as mk_prefill, and as slow (products on the CUDA cores: many times a decode
+ * step).  tokens: device int32 [B][n];
  * lens: the rows of each sequence in kv_cache, which here are its positions too.  Node i of sequence
  * b stands at position lens[b] + the number of its ancestors; its keys and values are written to
  * cache row lens[b] + i of every layer, for mk_cache_commit to keep or the next call to overwrite.
@@ -452,7 +454,8 @@ typedef struct mk_verify_shape {
  *   infinite, or only -inf; children of such a node are not accepted; -1 with n_path 0 for a
  *   sequence without nodes).
  * Requirements: vocab <= 2^20, B * n <= 65535; path, n_path and next_token overlap none of the
- * inputs.  Sums that a draw depends on are formed in 64 bits.  workspace: device scratch of
+ * inputs.  Sums that a draw depends on are formed in 64 bits; a probability below 2^-1000 times the row's
+ * largest counts as 0.  workspace: device scratch of
  * mk_tree_verify_workspace_bytes, 16-byte aligned, its contents do not matter; calls that share it
  * must not overlap (nor may replays of graphs that captured such calls).  Two launches. */
 size_t mk_tree_verify_workspace_bytes(int B, int n, int vocab);

@@ -19,11 +19,12 @@
 // the ancestor bits of every node, and V tiles that end the sequence.
 //
 // Bound.  With few rows per key memory: 16 sequences x 13 nodes over up to 1280 rows (32 KV heads of
-// 128) take 43 us, 4.7 TB/s.  With many the chain of a tile, scores - softmax - P - product: 8 x 256
-// nodes over 4096 rows (32 / 4 heads of 64) take 133 us, 550 TFLOP/s, with the exponential unit busy
-// for less than half of the time and the tensor cores for a third; 4 x 64 nodes over up to 32768 rows
-// (32 / 8 heads of 128) 120 us, 760 TFLOP/s for the rows that are there.  5 nodes over 551 rows: 7.5 us,
-// of which the loads' and the cluster's latencies are nearly all.
+// 128) take 42 to 48 us by their lengths, 4.2 to 4.8 TB/s.  With many the chain of a tile, scores -
+// softmax - P - product: 8 x 256 nodes over 4096 rows (32 / 4 heads of 64) take 132 us, 550 TFLOP/s, with
+// the exponential unit busy for less than half of the time and the tensor cores for a third; 4 x 64 nodes
+// over up to 32768 rows (32 / 8 heads of 128, fp16) 118 to 150 us, 610 to 770 TFLOP/s, by their lengths
+// and by the clock that the power limit leaves.  5 nodes over 551 rows: 7.5 us, 1 node 7.2, of which the
+// loads' and the cluster's latencies are nearly all.
 //
 // The keys of a (sequence, KV head, row tile) unit are split over a thread-block cluster, whose
 // blocks merge their partial results through distributed shared memory: no workspace, no
@@ -34,7 +35,9 @@
 // maximum that P is taken against is only moved when it grows by more than 2^8; fp16 takes P
 // times 2^7, so that small weights stay clear of fp16's subnormals (largest 2^15).  With fp32 q and o
 // (WIDE) q and P each enter their product as two 16-bit parts, the value's rounding and what that
-// left over, so that both products see 16 (bf16) or 22 (fp16) bits of them.
+// left over, so that both products see 16 (bf16) or 22 (fp16) bits of them.  That is twice the products,
+// and with heads of 128 one block per SM, whose chain nothing overlaps then: the cases above take 71,
+// 164, 273 and 8.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -16,9 +16,9 @@
 //
 // Bound: the walk's latency.  A pass over a row of 128255 words by 8 blocks takes 6 to 9 us, a third
 // of it exchange and control, the rest fp64 arithmetic at half its rate (16 blocks: 4 to 5).  16
-// sequences x 9 nodes of that size (bf16, sampled drafts) take 66 us, of which row_stats 15 and the
-// longest walk nearly all the rest; one chain of 5 (fp32, 128256 words) 17 us; 4 x 26 nodes of 65536
-// words without a draft 20 us.
+// sequences x 9 nodes of that size (bf16, sampled drafts) take 52 to 65 us by their drafts, of which
+// row_stats 15 and the longest walk nearly all the rest; one chain of 5 (fp32, 128256 words) 17 us; 4 x 26
+// nodes of 65536 words without a draft 20 us.  At temperature 0 no pass is left: 25, 7.5 and 14.5 us.
 //
 // Precision.  A draw from 1e5 words by cumulative sums meets a border within 1e-7 in about every
 // hundredth draw, so sums that decide a draw are formed in fp64 from exponentials good to 1e-13.

@@ -391,8 +391,9 @@ def mk_attention_debug_drop_unit(unit: int):
 
 # ---- speculative decoding: these take torch tensors and read sizes, strides and types off them.
 # Like torch's own operators they run on the current stream of the tensors' device unless they are
-# given one (0: the NULL stream).  A decoding loop makes these calls for kernels of a few microseconds, so the checks are kept
-# cheap: plain comparisons, and the shape structs packed instead of built field by field.
+# given one (0: the NULL stream).  A decoding loop makes these calls for kernels of a few
+# microseconds, so the checks are kept cheap: plain comparisons, and the shape structs packed instead
+# of built field by field.
 
 _TREE_SHAPE = struct.Struct("8i12q")
 _VERIFY_SHAPE = struct.Struct("4i4q")
